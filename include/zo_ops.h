@@ -198,6 +198,124 @@ int zo_op_lm_head_logprob_noalloc(const void* h, const void* E, const int32_t* t
                                   int32_t n_rows, int32_t vocab, int32_t d, int32_t dtype,
                                   float* logprob, int32_t impl, void* stream);
 
+/* ---- serving: a paged key/value cache and per-request adapters ------------------------
+ * Foreground requests share the probe's base weights and batches ("Inference-Native
+ * Zeroth-Order Optimization", abstract: co-batched foreground inference).  The calls below
+ * serve them over a cache of pages instead of one contiguous span per row, and under
+ * adapters of their own instead of one bank.
+ *
+ * The paged cache of a layer is n_slots = n_pages * page_size rows of
+ * 2 * n_kv_heads * head_dim elements, k then v (a row of zo_generate's cache); page p holds
+ * the rows p * page_size ..  page_size is a power of two from 8 to 256.  Request r's
+ * token at position i is in row block_table[r][i / page_size] * page_size + i % page_size.
+ * Lengths, tables and slots are device arrays that no call reads on the host: every call is
+ * asynchronous on stream and can be captured into a CUDA graph, whose replays read the
+ * arrays' new contents. */
+
+/* Block tables, slots and offsets of one step, from the requests' lengths before and after
+ * it.  Request r goes from old_lens[r] to new_lens[r] tokens: a longer request takes pages
+ * from the head of the ring of free pages, in request order, then block order; a shorter
+ * one (0: it ends) gives the pages past its new end back to the ring's tail in the same
+ * order.  Pages given back are not taken again in the same call.
+ *   old_lens, new_lens  dev int32 [n_rows]
+ *   block_table  dev int32 [n_rows x max_blocks]; entries of pages taken are written, all
+ *                others are left as they were (those past a request's end mean nothing)
+ *   free_ring    dev int32 [n_pages]: the count free pages are at (head + i) % n_pages
+ *   state        dev int32 [4]: head, count, -, -; read only
+ *   state_out    dev int32 [4]: head and count after the step, status, 0; must not be state.
+ *                So a call can be repeated with the same result; the next step passes this
+ *                step's state_out as its state
+ *   cu_new       dev int32 [n_rows + 1]: offsets of the new tokens, packed in request order
+ *   slot_map     dev int32 [max_tokens]: cache row of each packed new token, -1 behind the last
+ * Status 0: done.  Otherwise the step is refused as a whole -- no table or ring entry
+ * changes, cu_new is all 0, slot_map all -1, head and count stay -- with status > 0: so many
+ * pages are missing; -1: a length is negative or needs more than max_blocks pages; -2: more
+ * than max_tokens new tokens; -3: more pages come back than the ring has room for; -4: head
+ * or count is outside the ring.
+ * ZO_ERR_ARG on NULL pointers, sizes below 1 (n_rows, max_tokens: below 0), a page_size
+ * that is no power of two from 8 to 256, n_pages * page_size above 2^31 - 1 or state_out ==
+ * state. */
+int zo_op_block_tables(const int32_t* old_lens, const int32_t* new_lens, int32_t n_rows,
+                       int32_t page_size, int32_t* block_table, int32_t max_blocks,
+                       int32_t* free_ring, int32_t n_pages, const int32_t* state,
+                       int32_t* state_out, int32_t* cu_new, int32_t* slot_map,
+                       int32_t max_tokens, void* stream);
+
+/* Writes the packed rows' keys and values into the paged cache:
+ * cache[slot_map[t]] = qkv[t][n_heads * head_dim ..] (the k | v columns).
+ *   qkv       dev [n_tokens x ld_qkv] dtype, q | k | v per row as for zo_op_attention
+ *   slot_map  dev int32 [n_tokens]; rows whose slot is outside [0, n_slots) are not written
+ *   cache     dev [n_slots x 2 * n_kv_heads * head_dim] dtype
+ * When two rows name the same slot, which of them it ends up holding is not defined.
+ * ZO_ERR_ARG on NULL pointers, negative sizes, or ld_qkv < (n_heads + 2 n_kv_heads) *
+ * head_dim. */
+int zo_op_kv_write(const void* qkv, int64_t ld_qkv, const int32_t* slot_map, int32_t n_tokens,
+                   void* cache, int64_t n_slots, int32_t n_heads, int32_t n_kv_heads,
+                   int32_t head_dim, int32_t dtype, void* stream);
+
+/* Attention of new tokens over the paged cache: decode steps, chunks of long prompts and whole
+ * prompts in one packed batch.  Request r has lens[r] tokens in the cache, of which the last
+ * n = cu_new[r + 1] - cu_new[r] are its new ones; the query at row cu_new[r] + i sees the
+ * keys at positions 0 .. lens[r] - n + i:
+ *   out = softmax(q k^T / sqrt(head_dim)) v, query head h using kv head h / (H / Hkv).
+ *   q        dev [n_tokens x ld_q] dtype: the query heads are a row's first H * hd columns (so
+ *            the packed q|k|v rows can be passed as they are)
+ *   cache    dev [n_slots x 2 * Hkv * hd] dtype; the new tokens' rows must be in it already
+ *            (zo_op_kv_write).  Rows behind a request's end, in its last page too, are never
+ *            part of a result, whatever they hold
+ *   block_table dev int32 [n_rows x max_blocks];  cu_new dev int32 [n_rows + 1], non-decreasing
+ *            from 0;  lens dev int32 [n_rows]
+ *   out      dev [n_tokens x ld_out] dtype; rows at and behind cu_new[n_rows] are left as
+ *            they were
+ *   max_new  the most new tokens any request has (host): chooses the kernels, so that a
+ *            decode step launches only the one for single tokens.  A request with more is
+ *            still computed, more slowly
+ *   ws       dev, 16-byte aligned, >= zo_op_attention_paged_workspace(...) bytes; scratch, not
+ *            to be shared by calls that may run at the same time
+ *   impl     ZO_IMPL_TENSOR_CORES needs bf16, head_dim 64 or 128, at most 128 query heads per
+ *            kv head, 16-byte aligned pointers and strides that are multiples of 8 elements;
+ *            AUTO picks it then, else CUDA cores
+ * A request whose lens is below its new tokens or above max_blocks * page_size, or that names
+ * a page outside [0, n_slots / page_size) within its length, gets NaN rows; one whose rows are
+ * not inside [0, n_tokens) is left out.  A non-finite key or value can make every row of its
+ * own request NaN, also rows before it.
+ * ZO_ERR_ARG on NULL pointers, sizes below 1 (n_rows, n_tokens: below 0), n_heads not a
+ * multiple of n_kv_heads, strides below the row, a page_size that is no power of two from 8
+ * to 256, n_slots no multiple of page_size or above 2^31 - 1, or a workspace too small;
+ * ZO_ERR_UNSUPPORTED for head_dim other than 32, 64, 128, 256. */
+size_t zo_op_attention_paged_workspace(int32_t n_tokens, int32_t n_rows, int32_t n_heads,
+                                       int32_t n_kv_heads, int32_t head_dim, int32_t dtype);
+int zo_op_attention_paged(const void* q, int64_t ld_q, const void* cache, int64_t n_slots,
+                          const int32_t* block_table, int32_t max_blocks, int32_t page_size,
+                          const int32_t* cu_new, const int32_t* lens, int32_t n_rows,
+                          int32_t n_tokens, int32_t max_new, int32_t n_heads,
+                          int32_t n_kv_heads, int32_t head_dim, int32_t dtype, void* out,
+                          int64_t ld_out, void* ws, size_t ws_bytes, int32_t impl, void* stream);
+
+/* One linear layer for rows of many requests, each under an adapter of its own:
+ *   y[m] = act(x[m] W^T + b + scale[a] (x[m] A_a^T) B_a^T),   a = row_adapter[m],
+ * without forming any W + scale B A ("Inference-Native Zeroth-Order Optimization", abstract:
+ * factorised side states over frozen base weights; here one per request).
+ *   x    dev [M x K] dtype;  W dev [N x K] dtype;  bias dev float [N] or NULL
+ *   A    dev [n_adapters * rank x K] dtype: adapter a's shrink rows a * rank ..
+ *   B    dev [N x n_adapters * rank] dtype: adapter a's expand columns a * rank ..
+ *   row_adapter dev int32 [M]: -1 for no adapter; an id that is neither gives a NaN row
+ *   scale dev float [n_adapters]
+ *   y    dev [M x N] dtype, or with accumulate != 0 dev float [M x N] (+=; act must be none)
+ *   ws   dev, 256-byte aligned, >= zo_op_linear_adapters_workspace(...) bytes; scratch, not to
+ *        be shared by calls that may run at the same time
+ *   impl ZO_IMPL_TENSOR_CORES needs dtype bf16, K, N and n_adapters * rank multiples of 8 and
+ *        16-byte aligned pointers; AUTO picks it then, else CUDA cores
+ * M = 0 is a no-op.  ZO_ERR_ARG on NULL pointers, negative or empty sizes, rank above 256 or
+ * n_adapters * rank above 65536, an unknown act, or a workspace too small or not aligned. */
+size_t zo_op_linear_adapters_workspace(int32_t M, int32_t N, int32_t K, int32_t n_adapters,
+                                       int32_t rank, int32_t dtype);
+int zo_op_linear_adapters(const void* x, const void* W, const float* bias, const void* A,
+                          const void* B, const int32_t* row_adapter, const float* scale,
+                          int32_t n_adapters, int32_t rank, void* y, int32_t M, int32_t N,
+                          int32_t K, int32_t dtype, int32_t act, int32_t accumulate, void* ws,
+                          size_t ws_bytes, int32_t impl, void* stream);
+
 /* Synchronise the device and return the tensor-core kernels' error word:
  * 0 when clean, bit 0 set when a bounded wait inside a kernel expired (the
  * kernel then stopped early and its output is invalid), -1 when the device

@@ -178,6 +178,41 @@ bool launch_attention_tc(const AttnArgs& a, cudaStream_t st);       // tensor co
                                                                     // false if the tensor map fails
 int attention_tc_error_word();
 
+// ---- serving: paged cache ----------------------------------------------------------------
+// (zo_ops.h documents the arguments; page_size = 1 << page_shift)
+cudaError_t launch_block_tables(const int* old_lens, const int* new_lens, int R, int page_shift,
+                                int* table, int max_blocks, int* ring, int n_pages, const int* state,
+                                int* state_out, int* cu_new, int* slots, int max_tokens,
+                                cudaStream_t st);
+// kv: the first row's k columns; rows ld_bytes apart, row_bytes copied each
+cudaError_t launch_kv_write(const void* kv, long long ld_bytes, const int* slots, int n_tokens,
+                            void* cache, long long n_slots, int row_bytes, cudaStream_t st);
+struct PagedArgs {
+    const void* q; long long ld_q;          // [n_tokens x ld_q]
+    const void* cache; long long n_slots;   // [n_slots x 2 Hkv hd]
+    const int* block_table; int max_blocks, page_shift;
+    const int* cu_new; const int* lens;     // [n_rows + 1], [n_rows]
+    int n_rows, n_tokens, max_new;
+    int H, Hkv, g, hd;                      // g = H / Hkv
+    float scale;
+    int dtype;
+    void* out; long long ld_out;
+    void* ws;
+};
+cudaError_t launch_paged_attention(const PagedArgs& a, cudaStream_t st);   // CUDA cores
+
+// ---- serving: one adapter per row ----------------------------------------------------------
+struct AdapterArgs {
+    const void* x; const void* W; const float* bias; const void* A; const void* B;
+    const int* ids; const float* scale;
+    int n_adapters, rank;
+    void* y; int M, N, K;
+    int dtype, act, accumulate;
+    void* ws; size_t ws_bytes;
+};
+size_t adapter_workspace(int M, int N, int K, int n_adapters, int rank, int dtype);
+cudaError_t launch_linear_adapters_simt(const AdapterArgs& a, cudaStream_t st);
+
 // ---- objective, estimator, update ------------------------------------------------------
 void launch_lse_merge(const float* part_max, const float* part_sum, const float* tgt_logit,
                       int S, int n_tiles, float* logprob, cudaStream_t st);

@@ -36,6 +36,13 @@ bool use_tc(int32_t impl, int dtype) {
     if (impl == ZO_IMPL_CUDA_CORES) return false;
     return dtype == ZO_DTYPE_BF16;
 }
+
+// the exponent of a cache page size (8, 16, .. 256 tokens), or -1
+int page_shift(int32_t page_size) {
+    for (int s = 3; s <= 8; ++s)
+        if (page_size == 1 << s) return s;
+    return -1;
+}
 }  // namespace
 
 extern "C" {
@@ -282,6 +289,124 @@ int zo_op_rope_table(float* cos_t, float* sin_t, int32_t max_pos, int32_t head_d
         return ZO_ERR_ARG;
     launch_rope_table(cos_t, sin_t, max_pos, head_dim, theta, static_cast<cudaStream_t>(stream));
     return op_status();
+}
+
+int zo_op_block_tables(const int32_t* old_lens, const int32_t* new_lens, int32_t n_rows,
+                       int32_t page_size, int32_t* block_table, int32_t max_blocks,
+                       int32_t* free_ring, int32_t n_pages, const int32_t* state,
+                       int32_t* state_out, int32_t* cu_new, int32_t* slot_map,
+                       int32_t max_tokens, void* stream) {
+    const int shift = page_shift(page_size);
+    if (shift < 0 || n_rows < 0 || max_blocks < 1 || n_pages < 1 || max_tokens < 0) return ZO_ERR_ARG;
+    if (((int64_t)n_pages << shift) > 0x7fffffffLL) return ZO_ERR_ARG;
+    if (!free_ring || !state || !state_out || !cu_new || state == state_out) return ZO_ERR_ARG;
+    if (n_rows > 0 && (!old_lens || !new_lens || !block_table)) return ZO_ERR_ARG;
+    if (max_tokens > 0 && !slot_map) return ZO_ERR_ARG;
+    if (launch_block_tables(old_lens, new_lens, n_rows, shift, block_table, max_blocks, free_ring,
+                            n_pages, state, state_out, cu_new, slot_map, max_tokens,
+                            static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return op_fail("block table launch failed");
+    return ZO_OK;
+}
+
+int zo_op_kv_write(const void* qkv, int64_t ld_qkv, const int32_t* slot_map, int32_t n_tokens,
+                   void* cache, int64_t n_slots, int32_t n_heads, int32_t n_kv_heads,
+                   int32_t head_dim, int32_t dtype, void* stream) {
+    if (n_tokens < 0 || n_slots < 1 || n_heads < 0 || n_kv_heads < 1 || head_dim < 1) return ZO_ERR_ARG;
+    if (dtype != ZO_DTYPE_FP32 && dtype != ZO_DTYPE_BF16) return ZO_ERR_ARG;
+    const int64_t es = dtype == ZO_DTYPE_BF16 ? 2 : 4;
+    const int64_t q = (int64_t)n_heads * head_dim, kv = (int64_t)2 * n_kv_heads * head_dim;
+    if (ld_qkv < q + kv || kv * es > 0x7fffffffLL) return ZO_ERR_ARG;
+    if (n_tokens == 0) return ZO_OK;
+    if (!qkv || !slot_map || !cache) return ZO_ERR_ARG;
+    if (launch_kv_write(static_cast<const char*>(qkv) + q * es, ld_qkv * es, slot_map, n_tokens, cache,
+                        n_slots, (int)(kv * es), static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return op_fail("cache write launch failed");
+    return ZO_OK;
+}
+
+size_t zo_op_attention_paged_workspace(int32_t n_tokens, int32_t n_rows, int32_t n_heads,
+                                       int32_t n_kv_heads, int32_t head_dim, int32_t dtype) {
+    (void)n_tokens; (void)n_rows; (void)n_heads; (void)n_kv_heads; (void)head_dim; (void)dtype;
+    return 256;
+}
+
+int zo_op_attention_paged(const void* q, int64_t ld_q, const void* cache, int64_t n_slots,
+                          const int32_t* block_table, int32_t max_blocks, int32_t page_size,
+                          const int32_t* cu_new, const int32_t* lens, int32_t n_rows,
+                          int32_t n_tokens, int32_t max_new, int32_t n_heads,
+                          int32_t n_kv_heads, int32_t head_dim, int32_t dtype, void* out,
+                          int64_t ld_out, void* ws, size_t ws_bytes, int32_t impl, void* stream) {
+    const int shift = page_shift(page_size);
+    if (shift < 0 || n_rows < 0 || n_tokens < 0 || max_new < 0 || max_blocks < 1) return ZO_ERR_ARG;
+    if (n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads || head_dim < 1) return ZO_ERR_ARG;
+    if (dtype != ZO_DTYPE_FP32 && dtype != ZO_DTYPE_BF16) return ZO_ERR_ARG;
+    if (impl < ZO_IMPL_AUTO || impl > ZO_IMPL_TENSOR_CORES) return ZO_ERR_ARG;
+    if (ld_q < (int64_t)n_heads * head_dim || ld_out < (int64_t)n_heads * head_dim) return ZO_ERR_ARG;
+    if (n_slots < page_size || n_slots % page_size || n_slots > 0x7fffffffLL) return ZO_ERR_ARG;
+    if (head_dim != 32 && head_dim != 64 && head_dim != 128 && head_dim != 256)
+        return ZO_ERR_UNSUPPORTED;
+    if (n_kv_heads > 65535 || (int64_t)n_tokens * (n_heads / n_kv_heads) > 0x7fffffffLL)
+        return ZO_ERR_UNSUPPORTED;
+    if (n_rows == 0 || n_tokens == 0) return ZO_OK;
+    if (!q || !cache || !block_table || !cu_new || !lens || !out) return ZO_ERR_ARG;
+    if (!ws || reinterpret_cast<uintptr_t>(ws) % 16 ||
+        ws_bytes < zo_op_attention_paged_workspace(n_tokens, n_rows, n_heads, n_kv_heads, head_dim, dtype))
+        return ZO_ERR_ARG;
+    PagedArgs a;
+    memset(&a, 0, sizeof(a));
+    a.q = q; a.ld_q = ld_q;
+    a.cache = cache; a.n_slots = n_slots;
+    a.block_table = block_table; a.max_blocks = max_blocks; a.page_shift = shift;
+    a.cu_new = cu_new; a.lens = lens;
+    a.n_rows = n_rows; a.n_tokens = n_tokens; a.max_new = max_new;
+    a.H = n_heads; a.Hkv = n_kv_heads; a.g = n_heads / n_kv_heads; a.hd = head_dim;
+    a.scale = (float)(1.0 / std::sqrt((double)head_dim));
+    a.dtype = dtype == ZO_DTYPE_BF16 ? E_BF16 : E_F32;
+    a.out = out; a.ld_out = ld_out;
+    a.ws = ws;
+    if (impl == ZO_IMPL_TENSOR_CORES) return ZO_ERR_UNSUPPORTED;
+    if (launch_paged_attention(a, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return op_fail("paged attention launch failed");
+    return ZO_OK;
+}
+
+size_t zo_op_linear_adapters_workspace(int32_t M, int32_t N, int32_t K, int32_t n_adapters,
+                                       int32_t rank, int32_t dtype) {
+    if (M < 0 || N < 1 || K < 1 || n_adapters < 1 || rank < 1) return 0;
+    return adapter_workspace(M, N, K, n_adapters, rank, dtype == ZO_DTYPE_BF16 ? E_BF16 : E_F32);
+}
+
+int zo_op_linear_adapters(const void* x, const void* W, const float* bias, const void* A,
+                          const void* B, const int32_t* row_adapter, const float* scale,
+                          int32_t n_adapters, int32_t rank, void* y, int32_t M, int32_t N,
+                          int32_t K, int32_t dtype, int32_t act, int32_t accumulate, void* ws,
+                          size_t ws_bytes, int32_t impl, void* stream) {
+    if (M < 0 || N < 1 || K < 1 || n_adapters < 1 || rank < 1 || rank > 256) return ZO_ERR_ARG;
+    if ((int64_t)n_adapters * rank > 65536) return ZO_ERR_ARG;
+    if (dtype != ZO_DTYPE_FP32 && dtype != ZO_DTYPE_BF16) return ZO_ERR_ARG;
+    if (act != ZO_ACT_NONE && act != ZO_ACT_RELU) return ZO_ERR_ARG;
+    if (accumulate && act != ZO_ACT_NONE) return ZO_ERR_ARG;
+    if (impl < ZO_IMPL_AUTO || impl > ZO_IMPL_TENSOR_CORES) return ZO_ERR_ARG;
+    if (M == 0) return ZO_OK;
+    if (!x || !W || !A || !B || !row_adapter || !scale || !y) return ZO_ERR_ARG;
+    if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 ||
+        ws_bytes < zo_op_linear_adapters_workspace(M, N, K, n_adapters, rank, dtype))
+        return ZO_ERR_ARG;
+    if (M > 65535 * 64) return ZO_ERR_UNSUPPORTED;
+    AdapterArgs a;
+    memset(&a, 0, sizeof(a));
+    a.x = x; a.W = W; a.bias = bias; a.A = A; a.B = B;
+    a.ids = row_adapter; a.scale = scale;
+    a.n_adapters = n_adapters; a.rank = rank;
+    a.y = y; a.M = M; a.N = N; a.K = K;
+    a.dtype = dtype == ZO_DTYPE_BF16 ? E_BF16 : E_F32;
+    a.act = act; a.accumulate = accumulate;
+    a.ws = ws; a.ws_bytes = ws_bytes;
+    if (impl == ZO_IMPL_TENSOR_CORES) return ZO_ERR_UNSUPPORTED;
+    if (launch_linear_adapters_simt(a, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return op_fail("adapter linear launch failed");
+    return ZO_OK;
 }
 
 int64_t zo_op_set_wait_limit(int64_t cycles) {

@@ -7,6 +7,7 @@ the import of any entry point raises: there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Dict, List, Optional, Sequence
@@ -29,6 +30,7 @@ IMPL_AUTO, IMPL_CUDA_CORES, IMPL_TENSOR_CORES = 0, 1, 2
 
 c_void_p = ctypes.c_void_p
 c_int32 = ctypes.c_int32
+c_int64 = ctypes.c_int64
 c_uint32 = ctypes.c_uint32
 c_uint64 = ctypes.c_uint64
 
@@ -148,6 +150,21 @@ _SIGS = {
                                         c_void_p]),
     "zo_op_attention": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32,
                                   c_int32, c_int32, c_void_p, ctypes.c_size_t, c_int32, c_void_p]),
+    "zo_op_block_tables": (c_int32, [c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_int32,
+                                     c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_void_p,
+                                     c_int32, c_void_p]),
+    "zo_op_kv_write": (c_int32, [c_void_p, c_int64, c_void_p, c_int32, c_void_p, c_int64, c_int32,
+                                 c_int32, c_int32, c_int32, c_void_p]),
+    "zo_op_attention_paged_workspace": (ctypes.c_size_t, [c_int32] * 6),
+    "zo_op_attention_paged": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int32,
+                                        c_int32, c_void_p, c_void_p, c_int32, c_int32, c_int32,
+                                        c_int32, c_int32, c_int32, c_int32, c_void_p, c_int64,
+                                        c_void_p, ctypes.c_size_t, c_int32, c_void_p]),
+    "zo_op_linear_adapters_workspace": (ctypes.c_size_t, [c_int32] * 6),
+    "zo_op_linear_adapters": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                        c_void_p, c_int32, c_int32, c_void_p, c_int32, c_int32,
+                                        c_int32, c_int32, c_int32, c_int32, c_void_p,
+                                        ctypes.c_size_t, c_int32, c_void_p]),
     "zo_op_error_word": (c_int32, []),
     "zo_op_lm_head_noalloc_capacity": (ctypes.c_size_t, []),
     "zo_op_lm_head_logprob_noalloc": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int32,
@@ -663,6 +680,181 @@ def zo_op_lm_head_logprob_noalloc(h: torch.Tensor, E: torch.Tensor, targets: tor
     dtype = wl.DTYPE_BF16 if h.dtype == torch.bfloat16 else wl.DTYPE_FP32
     _check_op(lib().zo_op_lm_head_logprob_noalloc(_ptr(h), _ptr(E), _ptr(targets), S, E.shape[0], d,
                                                dtype, _ptr(out), impl, _stream()))
+    return out
+
+
+# ---- serving ops: a paged key/value cache and per-request adapters -----------------------
+
+_I32 = (torch.int32,)
+
+
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _on(name: str, t):
+    """The tensor's device as the current one: a call queues on that device's current stream,
+    whichever device the caller has current."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    return _HERE_ALREADY if t.device.index == torch.cuda.current_device() \
+        else torch.cuda.device(t.device)
+
+
+def _dtype_id(dt: torch.dtype) -> int:
+    return wl.DTYPE_BF16 if dt == torch.bfloat16 else wl.DTYPE_FP32
+
+
+def _rows(name: str, t: torch.Tensor, cols: int, dtypes) -> int:
+    """Row stride of a 2-d CUDA tensor with at least cols columns, contiguous within a row."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2 or t.shape[1] < cols or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [rows x >= {cols}], contiguous within a row")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
+    if t.shape[0] > 1 and t.stride(0) < cols:
+        raise ValueError(f"{name} has overlapping rows")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], cols)
+
+
+def zo_page_ring(n_pages: int, device="cuda"):
+    """(free_ring, state) of a pool whose n_pages pages are all free: the arrays
+    zo_op_block_tables takes pages from."""
+    return (torch.arange(n_pages, dtype=torch.int32, device=device),
+            torch.tensor([0, n_pages, 0, 0], dtype=torch.int32, device=device))
+
+
+def zo_op_block_tables(old_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
+                       free_ring: torch.Tensor, state: torch.Tensor, state_out: torch.Tensor,
+                       page_size: int, max_tokens: Optional[int] = None,
+                       cu_new: Optional[torch.Tensor] = None,
+                       slot_map: Optional[torch.Tensor] = None):
+    """(cu_new [R + 1], slot_map [max_tokens]) of a step that takes the requests from old_lens
+    to new_lens tokens; block_table, free_ring and state_out are updated in place.  Give
+    slot_map or max_tokens, the room for the step's new tokens."""
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be [requests x max_blocks]")
+    R, max_blocks = block_table.shape
+    with _on("old_lens", old_lens):
+        if cu_new is None:
+            cu_new = torch.empty(R + 1, dtype=torch.int32, device=old_lens.device)
+        if slot_map is None:
+            if max_tokens is None:
+                raise ValueError("give slot_map or max_tokens")
+            slot_map = torch.empty(max_tokens, dtype=torch.int32, device=old_lens.device)
+        _cuda_args({"old_lens": (R,), "new_lens": (R,), "free_ring": (None,), "state": (4,),
+                    "state_out": (4,), "cu_new": (R + 1,), "slot_map": (max_tokens,)},
+                   dict.fromkeys(("old_lens", "new_lens", "block_table", "free_ring", "state",
+                                  "state_out", "cu_new", "slot_map"), _I32),
+                   old_lens=old_lens, new_lens=new_lens, block_table=block_table,
+                   free_ring=free_ring, state=state, state_out=state_out, cu_new=cu_new,
+                   slot_map=slot_map)
+        _check_op(lib().zo_op_block_tables(
+            _ptr(old_lens), _ptr(new_lens), R, page_size, _ptr(block_table), max_blocks,
+            _ptr(free_ring), free_ring.numel(), _ptr(state), _ptr(state_out), _ptr(cu_new),
+            _ptr(slot_map), slot_map.numel(), _stream()))
+    return cu_new, slot_map
+
+
+def zo_op_kv_write(qkv: torch.Tensor, slot_map: torch.Tensor, cache: torch.Tensor, n_heads: int,
+                   n_kv_heads: int, head_dim: int) -> None:
+    """cache[slot_map[t]] = the k | v columns of qkv row t (rows whose slot is outside the cache
+    are left out).  qkv may be a row slice of a wider tensor."""
+    kv2 = 2 * n_kv_heads * head_dim
+    ld = _rows("qkv", qkv, n_heads * head_dim + kv2, _FLOATS)
+    _cuda_args({"cache": (None, kv2), "slot_map": (qkv.shape[0],)},
+               {"cache": (qkv.dtype,), "slot_map": _I32}, cache=cache, slot_map=slot_map)
+    if cache.device != qkv.device:
+        raise ValueError(f"cache is on {cache.device}, qkv on {qkv.device}")
+    with _on("qkv", qkv):
+        _check_op(lib().zo_op_kv_write(_ptr(qkv), ld, _ptr(slot_map), qkv.shape[0], _ptr(cache),
+                                       cache.shape[0], n_heads, n_kv_heads, head_dim,
+                                       _dtype_id(qkv.dtype), _stream()))
+
+
+def zo_op_attention_paged_workspace(n_tokens: int, n_rows: int, n_heads: int, n_kv_heads: int,
+                                    head_dim: int, dtype: torch.dtype = torch.bfloat16) -> int:
+    return int(lib().zo_op_attention_paged_workspace(n_tokens, n_rows, n_heads, n_kv_heads,
+                                                     head_dim, _dtype_id(dtype)))
+
+
+def zo_op_attention_paged(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
+                          page_size: int, cu_new: torch.Tensor, lens: torch.Tensor, max_new: int,
+                          n_heads: int, n_kv_heads: int, head_dim: int, impl: int = IMPL_AUTO,
+                          out: Optional[torch.Tensor] = None,
+                          ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of each request's new tokens (rows cu_new[r] .. of q) over its lens[r] cached
+    ones.  q and out may be row slices of wider tensors (q the packed q|k|v rows); rows of out
+    behind the last request are left as they were.  max_new: the most new tokens of a request."""
+    T = q.shape[0]
+    ld_q = _rows("q", q, n_heads * head_dim, _FLOATS)
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be [requests x max_blocks]")
+    R, max_blocks = block_table.shape
+    with _on("q", q):
+        if out is None:
+            out = torch.empty(T, n_heads * head_dim, dtype=q.dtype, device=q.device)
+        ld_out = _rows("out", out, n_heads * head_dim, (q.dtype,))
+        if out.shape[0] != T or out.device != q.device:
+            raise ValueError("out must have q's rows and device")
+        need = lib().zo_op_attention_paged_workspace(T, R, n_heads, n_kv_heads, head_dim,
+                                                     _dtype_id(q.dtype))
+        if ws is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        _cuda_args({"cache": (None, 2 * n_kv_heads * head_dim), "cu_new": (R + 1,), "lens": (R,),
+                    "ws": (None,)},
+                   {"cache": (q.dtype,), "block_table": _I32, "cu_new": _I32, "lens": _I32,
+                    "ws": (torch.uint8,)},
+                   cache=cache, block_table=block_table, cu_new=cu_new, lens=lens, ws=ws)
+        if cache.device != q.device:
+            raise ValueError(f"cache is on {cache.device}, q on {q.device}")
+        _check_op(lib().zo_op_attention_paged(
+            _ptr(q), ld_q, _ptr(cache), cache.shape[0], _ptr(block_table), max_blocks, page_size,
+            _ptr(cu_new), _ptr(lens), R, T, max_new, n_heads, n_kv_heads, head_dim,
+            _dtype_id(q.dtype), _ptr(out), ld_out, _ptr(ws), ws.numel(), impl, _stream()))
+    return out
+
+
+def zo_op_linear_adapters_workspace(M: int, N: int, K: int, n_adapters: int, rank: int,
+                                    dtype: torch.dtype = torch.bfloat16) -> int:
+    return int(lib().zo_op_linear_adapters_workspace(M, N, K, n_adapters, rank, _dtype_id(dtype)))
+
+
+def zo_op_linear_adapters(x: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                          row_adapter: torch.Tensor, scale: torch.Tensor,
+                          bias: Optional[torch.Tensor] = None, act: int = 0,
+                          accumulate: bool = False, out: Optional[torch.Tensor] = None,
+                          ws: Optional[torch.Tensor] = None, impl: int = IMPL_AUTO) -> torch.Tensor:
+    """act(x W^T + bias + scale[a] (x A_a^T) B_a^T) with a = row_adapter[m] per row (-1: none).
+    A is [n_adapters * rank x K], adapter a's rows from a * rank; B is [N x n_adapters * rank],
+    adapter a's columns from a * rank; accumulate adds to a float32 out."""
+    M, K = x.shape
+    N = W.shape[0]
+    n_adapters = scale.shape[0]
+    if n_adapters < 1 or A.shape[0] % n_adapters:
+        raise ValueError("A must have rank rows for each of scale's adapters")
+    rank = A.shape[0] // n_adapters
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    with _on("x", x):
+        if out is None:
+            out = torch.empty(M, N, dtype=x.dtype, device=x.device)
+        if ws is None:
+            need = lib().zo_op_linear_adapters_workspace(M, N, K, n_adapters, rank,
+                                                         _dtype_id(x.dtype))
+            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
+        _cuda_args({"x": (M, K), "W": (N, K), "A": (n_adapters * rank, K),
+                    "B": (N, n_adapters * rank), "row_adapter": (M,), "scale": (n_adapters,),
+                    "bias": (N,), "out": (M, N), "ws": (None,)},
+                   {"x": _FLOATS, "W": (x.dtype,), "A": (x.dtype,), "B": (x.dtype,),
+                    "row_adapter": _I32, "scale": (torch.float32,), "bias": (torch.float32,),
+                    "out": (torch.float32,) if accumulate else (x.dtype,), "ws": (torch.uint8,)},
+                   x=x, W=W, A=A, B=B, row_adapter=row_adapter, scale=scale, bias=bias, out=out,
+                   ws=ws)
+        _check_op(lib().zo_op_linear_adapters(
+            _ptr(x), _ptr(W), _ptr(bias), _ptr(A), _ptr(B), _ptr(row_adapter), _ptr(scale),
+            n_adapters, rank, _ptr(out), M, N, K, _dtype_id(x.dtype), act, int(accumulate),
+            _ptr(ws), ws.numel(), impl, _stream()))
     return out
 
 
