@@ -1,0 +1,692 @@
+// Attention of a few query rows per request over the paged cache (decode steps): bf16, head_dim
+// 64 or 128, on the tensor cores' warp-level path.
+//
+// A decode step reads every cached key and value once and computes 4 g flops per element, so
+// HBM bounds it and the products only have to keep out of the way.  That decides the form:
+//
+// * The work of a call is one line of units -- 16 keys (with their values) of one (request, tile
+//   of query rows, kv head) -- and every warp of the grid takes an equal stretch of that line,
+//   whatever lengths the requests have.  A warp works alone: its own ring of shared-memory
+//   stages, its own barriers, running maxima, sums and outputs, no block-wide synchronisation.
+//   An item cut by a stretch's end is written as a partial (m, l, o) and the pieces are added in
+//   key order by a small second kernel.
+// * One TMA copy brings a unit: 16 rows of a page, k and v, as a 4-d box (64 columns, rows,
+//   column halves, k/v), 128-byte-swizzled, so each warp has STAGES x 8 KB (head_dim 128) in
+//   flight and an SM 192 KB.
+// * The products are transposed so that no row is padding: S^T = K Q^T takes 16 keys as the
+//   16-row side and up to 8 query rows per 8-column block, O^T += V^T P^T takes 16 of the head's
+//   dims; P^T turns from accumulator to operand layout by an 8x8 transpose in registers
+//   (movmatrix).  With m16n8k16 the MMAs of a 64 KB round of an SM's warps take well under the
+//   time HBM needs for those 64 KB.
+// * Softmax statistics, outputs and partials are fp32; P is rounded to bf16 for its product, as
+//   the packed attention does (the sum l is of the unrounded values).
+// Keys a query may not see get probability exactly 0; value rows behind the tile's last key are
+// cleared in registers (0 x NaN would not be 0).
+#include <cuda.h>
+#include <float.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace zo {
+
+namespace {
+
+constexpr int WARPS = 8, THREADS = WARPS * 32;
+constexpr int UK = 16;                               // keys per unit
+constexpr int GROUPS = 1024;                         // prefix entries kept in shared memory
+constexpr int MAX_CTAS = 148;
+constexpr int MAX_WORKERS = MAX_CTAS * WARPS;
+constexpr long long WAIT_CYCLES = 4000000000ll;      // ~2 s: a copy that never lands
+constexpr uint32_t DRAIN_POLLS = 1u << 24;
+
+__device__ int g_step_error = 0;                     // bit 0: a bounded wait expired
+
+template <int HD>
+struct Geo {
+    static constexpr int NH = HD / 64;               // 64-column halves of a head
+    static constexpr int STAGE = UK * HD * 2 * 2;    // bytes of a unit: k and v
+    static constexpr int STAGES = HD == 128 ? 3 : 6;
+    static constexpr int SMEM = WARPS * STAGES * STAGE + 1024;
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(1000u)
+        : "memory");
+    return ok != 0;
+}
+// Bounded wait of a whole warp for a unit's copy.
+__device__ __forceinline__ bool wait_unit(uint32_t bar, uint32_t parity, long long limit) {
+    if (bar_try(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (;;) {
+        if (bar_try(bar, parity)) return true;
+        if (clock64() - t0 > limit) {
+            atomicOr(&g_step_error, 1);
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, const uint32_t* b) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// What this kernel takes of request r: its rows per kv head (new tokens x g), 0 when it is left
+// out or has none, and whether its length can be used.
+struct Req {
+    int start, rows, ctx;
+    bool bad;
+};
+__device__ __forceinline__ Req get_req(const PagedArgs& a, int r) {
+    Req q;
+    const int s = a.cu_new[r], e = a.cu_new[r + 1], len = a.lens[r];
+    const int n = e - s;
+    const bool in = s >= 0 && e >= s && e <= a.n_tokens;
+    q.start = s;
+    q.rows = in && n <= a.step_tokens ? n * a.g : 0;
+    q.bad = len < n || (long long)len > ((long long)a.max_blocks << a.page_shift);
+    q.ctx = len - n;
+    return q;
+}
+// Keys (the end) and units of tile t of a request's rows, RB rows to a tile.
+template <int RB>
+__device__ __forceinline__ int tile_keys(const PagedArgs& a, const Req& q, int t) {
+    return q.ctx + (min((t + 1) * RB, q.rows) - 1) / a.g + 1;
+}
+template <int RB>
+__device__ __forceinline__ int tile_units(const PagedArgs& a, const Req& q, int t) {
+    return q.bad ? 1 : (tile_keys<RB>(a, q, t) + UK - 1) / UK;
+}
+template <int RB>
+__device__ __forceinline__ long long req_units(const PagedArgs& a, int r) {
+    const Req q = get_req(a, r);
+    long long u = 0;
+    for (int t = 0; t * RB < q.rows; ++t) u += tile_units<RB>(a, q, t);
+    return u * a.Hkv;
+}
+
+// A place on the line of units.
+struct Cursor {
+    Req q;
+    int r, tile, head, unit, units;
+};
+// The next request from r on that has rows here (there is one: the stretch is not used up).
+__device__ __forceinline__ void seek_req(const PagedArgs& a, Cursor& c) {
+    c.q.rows = 0;
+    while (c.r < a.n_rows) {
+        c.q = get_req(a, c.r);
+        if (c.q.rows > 0) return;
+        ++c.r;
+    }
+}
+// To the next unit; `more`: the stretch goes on behind it.
+template <int RB>
+__device__ __forceinline__ void advance(const PagedArgs& a, Cursor& c, bool more) {
+    if (++c.unit < c.units) return;
+    c.unit = 0;
+    if (++c.head < a.Hkv) return;
+    c.head = 0;
+    if (!more) return;
+    if (++c.tile * RB >= c.q.rows) {
+        c.tile = 0;
+        ++c.r;
+        seek_req(a, c);
+    }
+    c.units = tile_units<RB>(a, c.q, c.tile);
+}
+
+// Slots of partial results, in the accumulator's own layout: slot 2 w: the piece with which worker
+// w's stretch begins (an item begun by an earlier worker); 2 w + 1: the one it ends with (an item
+// that goes on).  desc[w] describes the item of slot 2 w + 1.
+struct Desc {
+    int pieces;                       // workers w .. w + pieces - 1 hold a piece; 0: none
+    int start, row0, rows;            // first packed row; first and number of the request's rows
+    int kvh, pad[3];
+};
+template <int HD, int NB>
+struct Part {
+    float4 o[HD / 16][NB][32];
+    float m[NB * 8], l[NB * 8];
+};
+
+template <int HD, int NB>
+__device__ __forceinline__ void store_rows(const PagedArgs& a, int start, int row0, int rows, int kvh,
+                                           const float (*o)[NB][4], const float (*inv)[2], int lane) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int n = nb * 8 + 2 * (lane & 3) + e;
+            if (n >= rows) continue;
+            const int row = row0 + n;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                                 (size_t)(start + row / a.g) * a.ld_out +
+                                 (size_t)(kvh * a.g + row % a.g) * HD + (lane >> 2);
+#pragma unroll
+            for (int mt = 0; mt < HD / 16; ++mt) {
+                out[mt * 16] = __float2bfloat16_rn(o[mt][nb][e] * inv[nb][e]);
+                out[mt * 16 + 8] = __float2bfloat16_rn(o[mt][nb][2 + e] * inv[nb][e]);
+            }
+        }
+}
+
+template <int HD, int NB>
+__global__ void __launch_bounds__(THREADS, 1)
+    paged_step_kernel(const __grid_constant__ CUtensorMap map, PagedArgs a, int box_rows,
+                      Desc* __restrict__ desc, Part<HD, NB>* __restrict__ part) {
+    using G = Geo<HD>;
+    constexpr int RB = NB * 8, NH = G::NH, STAGES = G::STAGES;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t bars[WARPS * STAGES];
+    __shared__ long long cum[GROUPS + 1];
+    __shared__ long long wsum[WARPS];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t ring = ((smem_u32(raw) + 1023u) & ~1023u) + (uint32_t)(warp * STAGES * G::STAGE);
+    const uint32_t bar0 = smem_u32(bars + warp * STAGES);
+    if (lane == 0)
+        for (int s = 0; s < STAGES; ++s)
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar0 + 8u * s));
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    grid_dep_launch();                                // the joining kernel may be scheduled
+
+    // prefix sums of the requests' units, in groups of c requests
+    const int c = (a.n_rows + GROUPS - 1) / GROUPS;
+    const int groups = (a.n_rows + c - 1) / c;
+    long long base = 0;
+    for (int g0 = 0; g0 < groups; g0 += THREADS) {
+        const int gi = g0 + tid;
+        long long u = 0;
+        if (gi < groups)
+            for (int r = gi * c; r < min(a.n_rows, (gi + 1) * c); ++r) u += req_units<RB>(a, r);
+        long long incl = u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) wsum[warp] = incl;
+        __syncthreads();
+        long long before = 0, total = 0;
+        for (int w = 0; w < WARPS; ++w) {
+            if (w < warp) before += wsum[w];
+            total += wsum[w];
+        }
+        if (gi < groups) cum[gi + 1] = base + before + incl;
+        base += total;
+        __syncthreads();
+    }
+    if (tid == 0) cum[0] = 0;
+    __syncthreads();
+    const long long L = base;
+    const int workers = gridDim.x * WARPS, w = blockIdx.x * WARPS + warp;
+    const long long stretch = (L + workers - 1) / workers;      // units per worker
+    const long long u0 = stretch * w, u1 = min(L, u0 + stretch);
+    if (lane == 0) desc[w].pieces = 0;
+    if (u0 >= u1) return;                             // nothing to do, nothing in flight
+
+    Cursor con;
+    {
+        int lo = 0, hi = groups;                      // the last group with cum <= u0
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (cum[mid] <= u0) lo = mid;
+            else hi = mid;
+        }
+        long long rest = u0 - cum[lo];
+        con.r = lo * c;
+        for (;; ++con.r) {                            // within the group
+            const long long u = c == 1 ? LLONG_MAX : req_units<RB>(a, con.r);
+            if (rest < u) break;
+            rest -= u;
+        }
+        con.q = get_req(a, con.r);
+        con.tile = 0;
+        for (;;) {
+            con.units = tile_units<RB>(a, con.q, con.tile);
+            const long long u = (long long)con.units * a.Hkv;
+            if (rest < u) break;
+            rest -= u;
+            ++con.tile;
+        }
+        con.head = (int)(rest / con.units);
+        con.unit = (int)(rest % con.units);
+    }
+    Cursor pro = con;
+
+    // ---- producer side of the warp: unit `pro` into stage ps ----
+    const int n_pages = (int)(a.n_slots >> a.page_shift);
+    int ids = 0, ids_at = -1, ids_r = -1;             // 32 table entries, one per lane
+    uint32_t bad_stage = 0;
+    auto page_of = [&](int idx) {
+        if (ids_r != pro.r || idx < ids_at || idx >= ids_at + 32) {
+            ids_r = pro.r;
+            ids_at = idx;
+            ids = idx + lane < a.max_blocks ? a.block_table[(size_t)pro.r * a.max_blocks + idx + lane] : -1;
+        }
+        return __shfl_sync(0xffffffffu, ids, idx - ids_at);
+    };
+    auto issue = [&](int ps) {
+        const uint32_t dst = ring + (uint32_t)(ps * G::STAGE), bar = bar0 + 8u * ps;
+        const int kbase = pro.unit * UK;
+        uint32_t bytes = 0;
+        int row[2] = {-1, -1};
+        bool bad = pro.q.bad;
+        if (!bad) {
+            const int kend = tile_keys<RB>(a, pro.q, pro.tile);
+            const int subs = UK / box_rows;           // boxes per unit: 1, or 2 with pages of 8
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int k = kbase + s * box_rows;
+                if (s < subs && k < kend) {
+                    const int page = page_of(k >> a.page_shift);
+                    if ((unsigned)page < (unsigned)n_pages) {
+                        row[s] = (page << a.page_shift) + (k & ((1 << a.page_shift) - 1));
+                        bytes += (uint32_t)(box_rows * HD * 4);
+                    } else {
+                        bad = true;
+                    }
+                }
+            }
+        }
+        bad_stage = bad ? bad_stage | (1u << ps) : bad_stage & ~(1u << ps);
+        if (lane == 0) {
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                         : "memory");
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                if (row[s] >= 0)
+                    asm volatile(
+                        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst + (uint32_t)(s * box_rows * HD * 4)),
+                        "l"(reinterpret_cast<uint64_t>(&map)), "r"(bar), "r"(0), "r"(row[s]),
+                        "r"(pro.head * NH), "r"(0)
+                        : "memory");
+        }
+    };
+    long long issued = u0;
+    for (int s = 0; s < STAGES && issued < u1; ++s) {
+        issue(s);
+        ++issued;
+        advance<RB>(a, pro, issued < u1);
+    }
+
+    // ---- consumer side ----
+    const float sl2 = a.scale * 1.4426950408889634f;
+    // lane-dependent parts of the operand addresses: k rows by (lane & 7) + 8 * bit 3, value rows
+    // by (lane & 7) + 8 * bit 4; rows of 128 bytes, 16-byte chunks swizzled by the row
+    const uint32_t half_st = (uint32_t)box_rows * 128u;          // between column halves
+    const uint32_t v_st = half_st * NH;                          // from k to v
+    const uint32_t sub_st = box_rows == 16 ? 1024u : 2u * v_st;  // between the two 8-row groups
+    const uint32_t k_row = (uint32_t)(lane & 7) * 128u + ((lane >> 3) & 1) * sub_st;
+    const uint32_t v_row = v_st + (uint32_t)(lane & 7) * 128u + (lane >> 4) * sub_st;
+    const uint32_t k_chunk = lane >> 4, v_chunk = (lane >> 3) & 1, swz = lane & 7;
+
+    uint32_t qf[HD / 16][NB][2];
+    float o[HD / 16][NB][4], m[NB][2], l[NB][2];
+    int lim[NB][2], kend = 0, first_unit = 0;
+    bool bad = false, fresh = true, alive = true;
+    int stage = 0;
+    uint32_t phase = 0;
+    for (long long u = u0; u < u1; ++u) {
+        if (fresh) {                                  // a new item: its query rows and masks
+            fresh = false;
+            first_unit = con.unit;
+            bad = con.q.bad;
+            kend = con.q.bad ? 0 : tile_keys<RB>(a, con.q, con.tile);
+            const int row0 = con.tile * RB;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const int row = row0 + nb * 8 + (lane >> 2);
+                const bool live = row < con.q.rows;
+                const int rr = live ? row : row0;
+                const uint32_t* q = reinterpret_cast<const uint32_t*>(
+                    static_cast<const __nv_bfloat16*>(a.q) + (size_t)(con.q.start + rr / a.g) * a.ld_q +
+                    (size_t)(con.head * a.g + rr % a.g) * HD + 2 * (lane & 3));
+#pragma unroll
+                for (int kk = 0; kk < HD / 16; ++kk) {
+                    qf[kk][nb][0] = live ? __ldg(q + kk * 8) : 0u;
+                    qf[kk][nb][1] = live ? __ldg(q + kk * 8 + 4) : 0u;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int n = row0 + nb * 8 + 2 * (lane & 3) + e;
+                    lim[nb][e] = n < con.q.rows ? con.q.ctx + n / a.g + 1 : kend;
+                    m[nb][e] = -FLT_MAX;
+                    l[nb][e] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int mt = 0; mt < HD / 16; ++mt)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[mt][nb][e] = 0.f;
+        }
+        if (!wait_unit(bar0 + 8u * stage, phase, WAIT_CYCLES)) {
+            alive = false;
+            break;
+        }
+        bad |= (bad_stage >> stage) & 1u;
+        const uint32_t at = ring + (uint32_t)(stage * G::STAGE);
+        const int kbase = con.unit * UK;
+        float s[NB][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[nb][e] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk) {
+            uint32_t kf[4];
+            const uint32_t ch = (kk & 3) * 2 + k_chunk;
+            ldsm4(kf, at + k_row + (kk >> 2) * half_st + ((ch ^ swz) << 4));
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816(s[nb], kf, qf[kk][nb]);
+        }
+        const int left = kend - kbase;                // keys of the unit that exist for the tile
+        uint32_t pf[NB][2];
+        bool moved = false;
+        float alpha[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int key = kbase + (lane >> 2) + (e >> 1) * 8;
+                if (key >= min(lim[nb][e & 1], kend)) s[nb][e] = -INFINITY;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float mx = fmaxf(s[nb][e], s[nb][e + 2]);
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                const float mn = fmaxf(m[nb][e], mx);
+                alpha[nb][e] = ex2((m[nb][e] - mn) * sl2);
+                moved |= mn > m[nb][e];
+                m[nb][e] = mn;
+                const float ms = mn * sl2;
+                s[nb][e] = ex2(fmaf(s[nb][e], sl2, -ms));
+                s[nb][e + 2] = ex2(fmaf(s[nb][e + 2], sl2, -ms));
+                l[nb][e] = l[nb][e] * alpha[nb][e] + (s[nb][e] + s[nb][e + 2]);
+            }
+            pf[nb][0] = transpose8x8(pack2(s[nb][0], s[nb][1]));
+            pf[nb][1] = transpose8x8(pack2(s[nb][2], s[nb][3]));
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+            for (int mt = 0; mt < HD / 16; ++mt)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[mt][nb][e] *= alpha[nb][e & 1];
+        }
+        // value rows behind the last key: cleared, the two keys of a register one by one
+        const int k2 = 2 * (lane & 3);
+        const uint32_t keep0 = (k2 < left ? 0xffffu : 0u) | (k2 + 1 < left ? 0xffff0000u : 0u);
+        const uint32_t keep1 = (k2 + 8 < left ? 0xffffu : 0u) | (k2 + 9 < left ? 0xffff0000u : 0u);
+#pragma unroll
+        for (int mt = 0; mt < HD / 16; ++mt) {
+            uint32_t vf[4];
+            const uint32_t ch = (mt & 3) * 2 + v_chunk;
+            ldsm4t(vf, at + v_row + (mt >> 2) * half_st + ((ch ^ swz) << 4));
+            if (left < UK) {
+                vf[0] &= keep0;
+                vf[1] &= keep0;
+                vf[2] &= keep1;
+                vf[3] &= keep1;
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816(o[mt][nb], vf, pf[nb]);
+        }
+        __syncwarp();                                 // every lane has read the stage
+        if (issued < u1) {
+            issue(stage);
+            ++issued;
+            advance<RB>(a, pro, issued < u1);
+        }
+        if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+        }
+
+        const bool item_end = con.unit + 1 == con.units;
+        if (item_end || u + 1 == u1) {
+            fresh = true;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], d);
+                    if (bad) l[nb][e] = __int_as_float(0x7fc00000);
+                }
+            const int row0 = con.tile * RB, rows = min(RB, con.q.rows - row0);
+            if (first_unit == 0 && item_end) {
+                float inv[NB][2];
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) inv[nb][e] = 1.f / l[nb][e];
+                store_rows<HD, NB>(a, con.q.start, row0, rows, con.head, o, inv, lane);
+            } else {
+                Part<HD, NB>& p = part[2 * w + (first_unit == 0 ? 1 : 0)];
+#pragma unroll
+                for (int mt = 0; mt < HD / 16; ++mt)
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+                        p.o[mt][nb][lane] = make_float4(o[mt][nb][0], o[mt][nb][1], o[mt][nb][2], o[mt][nb][3]);
+                if (lane < 4)
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            p.m[nb * 8 + 2 * lane + e] = m[nb][e];
+                            p.l[nb * 8 + 2 * lane + e] = l[nb][e];
+                        }
+                if (first_unit == 0 && lane == 0) {
+                    // the item's last unit is (units - 1) behind its first, which is u - unit
+                    const long long last = u - con.unit + con.units - 1;
+                    Desc d;
+                    d.pieces = (int)(last / stretch) - w + 1;
+                    d.start = con.q.start;
+                    d.row0 = row0;
+                    d.rows = rows;
+                    d.kvh = con.head;
+                    desc[w] = d;
+                }
+            }
+        }
+        advance<RB>(a, con, u + 1 < u1);
+    }
+    if (!alive) {
+        // the copies still in flight land (or the bound ends) before the memory goes away
+        const int n = (int)min((long long)STAGES, issued - u0);
+        for (int s = 0; s < n; ++s) {
+            const uint32_t ph = (uint32_t)(((issued - u0 - 1 - s) / STAGES) & 1);
+            const uint32_t bar = bar0 + 8u * (uint32_t)((issued - u0 - 1 - s) % STAGES);
+            for (uint32_t i = 0; i < DRAIN_POLLS && !bar_try(bar, ph); ++i) __nanosleep(128);
+        }
+    }
+}
+
+// Adds the pieces of the item that worker w's stretch ended inside, in key order: one warp per
+// worker, in the partials' own layout.
+template <int HD, int NB>
+__global__ void __launch_bounds__(128) paged_step_join_kernel(PagedArgs a, const Desc* __restrict__ desc,
+                                                              const Part<HD, NB>* __restrict__ part,
+                                                              int workers) {
+    grid_dep_wait();
+    const int w = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (w >= workers) return;
+    const Desc d = desc[w];
+    if (d.pieces <= 0) return;
+    const float sl2 = a.scale * 1.4426950408889634f;
+    float o[HD / 16][NB][4], m[NB][2], l[NB][2];
+    const int c = 2 * (lane & 3);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            m[nb][e] = -FLT_MAX;
+            l[nb][e] = 0.f;
+        }
+    for (int i = 0; i < d.pieces; ++i) {
+        const Part<HD, NB>& p = part[2 * (w + i) + (i == 0 ? 1 : 0)];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) m[nb][e] = fmaxf(m[nb][e], p.m[nb * 8 + c + e]);
+    }
+#pragma unroll
+    for (int mt = 0; mt < HD / 16; ++mt)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[mt][nb][e] = 0.f;
+    for (int i = 0; i < d.pieces; ++i) {
+        const Part<HD, NB>& p = part[2 * (w + i) + (i == 0 ? 1 : 0)];
+        float f[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                f[nb][e] = ex2((p.m[nb * 8 + c + e] - m[nb][e]) * sl2);
+                l[nb][e] += f[nb][e] * p.l[nb * 8 + c + e];
+            }
+#pragma unroll
+        for (int mt = 0; mt < HD / 16; ++mt)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const float4 v = p.o[mt][nb][lane];
+                o[mt][nb][0] = fmaf(f[nb][0], v.x, o[mt][nb][0]);
+                o[mt][nb][1] = fmaf(f[nb][1], v.y, o[mt][nb][1]);
+                o[mt][nb][2] = fmaf(f[nb][0], v.z, o[mt][nb][2]);
+                o[mt][nb][3] = fmaf(f[nb][1], v.w, o[mt][nb][3]);
+            }
+    }
+    float inv[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) inv[nb][e] = 1.f / l[nb][e];
+    store_rows<HD, NB>(a, d.start, d.row0, d.rows, d.kvh, o, inv, lane);
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn() {
+    static const EncodeTiledFn fn = []() -> EncodeTiledFn {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<EncodeTiledFn>(p);
+        return nullptr;
+    }();
+    return fn;
+}
+
+// The cache [n_slots][2][Hkv][HD] as (64 columns, rows, column halves of all heads, k/v): a box of
+// 64 x rows x HD/64 x 2 is one head's keys and values of `rows` consecutive cache rows.
+bool cache_map(CUtensorMap* m, const PagedArgs& a, int rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t kv = (cuuint64_t)a.Hkv * a.hd * 2;          // bytes of a row's keys
+    const cuuint64_t dims[4] = {64, (cuuint64_t)a.n_slots, (cuuint64_t)(a.Hkv * a.hd / 64), 2};
+    const cuuint64_t strides[3] = {2 * kv, 128, kv};
+    const cuuint32_t box[4] = {64, (cuuint32_t)rows, (cuuint32_t)(a.hd / 64), 2};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.cache), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int HD, int NB>
+cudaError_t launch_step(const PagedArgs& a, cudaStream_t st) {
+    CUtensorMap map;
+    const int box_rows = min(UK, 1 << a.page_shift);
+    if (!cache_map(&map, a, box_rows)) return cudaErrorNotSupported;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(paged_step_kernel<HD, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Geo<HD>::SMEM);
+    if (e != cudaSuccess) return e;
+    const int grid = min(sms, MAX_CTAS);
+    Desc* desc = static_cast<Desc*>(a.ws);
+    auto* part = reinterpret_cast<Part<HD, NB>*>(static_cast<char*>(a.ws) + MAX_WORKERS * sizeof(Desc));
+    paged_step_kernel<HD, NB><<<grid, THREADS, Geo<HD>::SMEM, st>>>(map, a, box_rows, desc, part);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int workers = grid * WARPS;
+    return launch_pdl(paged_step_join_kernel<HD, NB>, dim3((workers + 3) / 4), dim3(128), 0, st, a,
+                      static_cast<const Desc*>(desc), static_cast<const Part<HD, NB>*>(part), workers);
+}
+
+}  // namespace
+
+size_t paged_step_workspace(int hd) {
+    const size_t p = hd == 128 ? sizeof(Part<128, 2>) : sizeof(Part<64, 2>);
+    return MAX_WORKERS * (sizeof(Desc) + 2 * p);
+}
+
+bool paged_tc_supported(const PagedArgs& a) {
+    const uintptr_t mix = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.cache) |
+                          reinterpret_cast<uintptr_t>(a.out);
+    return a.dtype == E_BF16 && (a.hd == 64 || a.hd == 128) && a.g <= 128 && mix % 16 == 0 &&
+           a.ld_q % 8 == 0 && a.ld_out % 8 == 0;
+}
+
+cudaError_t launch_paged_step(const PagedArgs& a, cudaStream_t st) {
+    if (a.n_tokens <= 0 || a.n_rows <= 0) return cudaSuccess;
+    const bool one = (long long)a.max_new * a.g <= 8;
+    if (a.hd == 128) return one ? launch_step<128, 1>(a, st) : launch_step<128, 2>(a, st);
+    return one ? launch_step<64, 1>(a, st) : launch_step<64, 2>(a, st);
+}
+
+int paged_step_error_word() {
+    int v = 0;
+    const int zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_step_error, sizeof(int)) != cudaSuccess) return -1;
+    cudaMemcpyToSymbol(g_step_error, &zero, sizeof(int));
+    return v;
+}
+
+}  // namespace zo

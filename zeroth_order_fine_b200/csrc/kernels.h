@@ -198,8 +198,14 @@ struct PagedArgs {
     int dtype;
     void* out; long long ld_out;
     void* ws;
+    int step_tokens;                        // requests of at most so many new tokens take the
+                                            // decode-step kernel
 };
 cudaError_t launch_paged_attention(const PagedArgs& a, cudaStream_t st);   // CUDA cores
+bool paged_tc_supported(const PagedArgs& a);                               // bf16, head_dim 64 or 128
+cudaError_t launch_paged_step(const PagedArgs& a, cudaStream_t st);
+size_t paged_step_workspace(int hd);
+int paged_step_error_word();
 
 // ---- serving: one adapter per row ----------------------------------------------------------
 struct AdapterArgs {

@@ -327,8 +327,9 @@ int zo_op_kv_write(const void* qkv, int64_t ld_qkv, const int32_t* slot_map, int
 
 size_t zo_op_attention_paged_workspace(int32_t n_tokens, int32_t n_rows, int32_t n_heads,
                                        int32_t n_kv_heads, int32_t head_dim, int32_t dtype) {
-    (void)n_tokens; (void)n_rows; (void)n_heads; (void)n_kv_heads; (void)head_dim; (void)dtype;
-    return 256;
+    (void)n_tokens; (void)n_rows; (void)n_heads; (void)n_kv_heads;
+    if (dtype != ZO_DTYPE_BF16 || (head_dim != 64 && head_dim != 128)) return 256;
+    return paged_step_workspace(head_dim);
 }
 
 int zo_op_attention_paged(const void* q, int64_t ld_q, const void* cache, int64_t n_slots,
@@ -365,9 +366,14 @@ int zo_op_attention_paged(const void* q, int64_t ld_q, const void* cache, int64_
     a.dtype = dtype == ZO_DTYPE_BF16 ? E_BF16 : E_F32;
     a.out = out; a.ld_out = ld_out;
     a.ws = ws;
+    a.step_tokens = 0x7fffffff;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (impl != ZO_IMPL_CUDA_CORES && paged_tc_supported(a)) {
+        if (launch_paged_step(a, st) != cudaSuccess) return op_fail("paged attention launch failed");
+        return ZO_OK;
+    }
     if (impl == ZO_IMPL_TENSOR_CORES) return ZO_ERR_UNSUPPORTED;
-    if (launch_paged_attention(a, static_cast<cudaStream_t>(stream)) != cudaSuccess)
-        return op_fail("paged attention launch failed");
+    if (launch_paged_attention(a, st) != cudaSuccess) return op_fail("paged attention launch failed");
     return ZO_OK;
 }
 
@@ -419,8 +425,9 @@ int zo_op_error_word(void) {
     if (cudaDeviceSynchronize() != cudaSuccess) return -1;
     const int v = gemm_tc_error_word();
     const int w = attention_tc_error_word();
-    if (v < 0 || w < 0) return -1;
-    return v | w;
+    const int s = paged_step_error_word();
+    if (v < 0 || w < 0 || s < 0) return -1;
+    return v | w | s;
 }
 
 int zo_debug_build(void) {
