@@ -3,8 +3,7 @@
 // sizes the tensor-core kernels do not take).
 #include <float.h>
 
-#include "common.cuh"
-#include "kernels.h"
+#include "paged.cuh"
 
 namespace zo {
 
@@ -338,7 +337,36 @@ cudaError_t launch_paged_hd(const PagedArgs& a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn() {
+    static const EncodeTiledFn fn = []() -> EncodeTiledFn {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<EncodeTiledFn>(p);
+        return nullptr;
+    }();
+    return fn;
+}
+
 }  // namespace
+
+bool paged_cache_map(CUtensorMap* m, const PagedArgs& a, int rows, int halves, int kvs) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t kv = (cuuint64_t)a.Hkv * a.hd * 2;          // bytes of a row's keys
+    const cuuint64_t dims[4] = {64, (cuuint64_t)a.n_slots, (cuuint64_t)(a.Hkv * a.hd / 64), 2};
+    const cuuint64_t strides[3] = {2 * kv, 128, kv};
+    const cuuint32_t box[4] = {64, (cuuint32_t)rows, (cuuint32_t)halves, (cuuint32_t)kvs};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.cache), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 cudaError_t launch_block_tables(const int* old_lens, const int* new_lens, int R, int page_shift,
                                 int* table, int max_blocks, int* ring, int n_pages, const int* state,

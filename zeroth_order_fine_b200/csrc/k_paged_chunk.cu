@@ -1,0 +1,663 @@
+// Attention of chunks of new tokens over the paged cache on the 5th-generation tensor cores: bf16,
+// head_dim 64 or 128.
+//
+// 4 hd flops per (query row, key) against 4 hd bytes per key and 256 rows: the tensor cores and
+// the exponentials bound it, HBM only when a chunk is short.  A work item is (256 query rows of one
+// request and kv head -- new tokens x the g heads that share it, token-major -- and that head's
+// keys); it is processed as two row tiles A and B of 128 against each 128-key unit, so that a key
+// tile fetched once serves 256 rows.  The units of all items form one line, cut into equal
+// stretches, one per SM; an item cut by a stretch's end is written as partial (m, l, o) and joined
+// by a second kernel in key order.
+//   warp 0       TMA producer: keys and values of a unit, page by page, into a ring of tiles; one
+//                box (64 columns of up to 128 rows) per lane, so the table lookups run in parallel
+//   warp 1       TMEM allocator and the single thread that issues tcgen05.mma:
+//                  S_t = Q_t K^T  (M 128, N 128, K hd), O_t (+)= P_t V (A from TMEM, N hd)
+//                in the order P_A V, Q_A K, P_B V, Q_B K: while one tile's softmax runs, the tensor
+//                cores work for the other
+//   warps 4..7   softmax of tile A, one row per thread (= its TMEM lane), 8..11 of tile B:
+//                P = exp2(S c - m) in bf16 back into TMEM over S's own columns (head_dim 128 fills
+//                the 512 columns with S_A S_B O_A O_B), so S_t of the next unit waits for P_t V
+// The running reference m of a row moves only when its maximum grows by more than 2^8: sums and
+// outputs stay exact in fp32 (P up to 2^8, the same relative rounding) and O is rarely rescaled.
+// Keys a row may not see get probability exactly 0.  Value rows behind the item's last key (the
+// rest of a page, or what an earlier tile left) are not multiplied: the product takes the 16-key
+// steps that hold keys, and the rest of the last step is cleared in shared memory.
+// Every wait is bounded; on expiry the kernel records the error word, lets what it issued land,
+// frees its tensor memory and returns.
+#include <float.h>
+
+#include "paged.cuh"
+
+namespace zo {
+
+namespace {
+
+constexpr int RB = 256, UK = 128;                    // rows of an item, keys of a unit
+constexpr int THREADS = 384;
+constexpr int ATOM = 128 * 128;                      // 64 columns of 128 rows
+constexpr int GROUPS = 1024;
+constexpr int MAX_CTAS = 148;
+constexpr long long WAIT_CYCLES = 4000000000ll;
+constexpr uint32_t DRAIN_POLLS = 1u << 24;
+constexpr uint32_t IDESC_QK = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(UK >> 3) << 17) |
+                              ((uint32_t)(128 >> 4) << 24);
+using Line = PagedLine<true, RB, UK>;
+
+__device__ int g_chunk_error = 0;
+
+template <int HD>
+struct Geo {
+    static constexpr int NA = HD / 64;               // column halves
+    static constexpr int TILE = NA * ATOM;           // bytes of 128 rows of q, k or v
+    static constexpr int STAGES = HD == 128 ? 5 : 8;
+    static constexpr int TAIL = 512;
+    static constexpr int SMEM = (2 + STAGES) * TILE + 1024 + TAIL;
+    static constexpr uint32_t IDESC_PV = (IDESC_QK & ~(0x3Fu << 17)) | ((uint32_t)(HD >> 3) << 17) |
+                                         (1u << 16);
+};
+
+template <int HD>
+struct Part {                                        // one piece of an item
+    float4 o[HD / 4][RB];
+    float m[RB], l[RB];
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// K-major operand: 128-byte rows in 8-row groups of 1024 bytes, 128-byte swizzle
+__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1u << 16) | ((uint64_t)(1024u >> 4) << 32) |
+           ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+// MN-major operand (values as loaded): 64-column blocks ATOM apart
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((uint32_t)ATOM >> 4) << 16) |
+           ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(1000u)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_f) {
+    if (bar_try(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (;;) {
+        if (bar_try(bar, parity)) return true;
+        if (*abort_f) return false;
+        if (clock64() - t0 > WAIT_CYCLES) {
+            *abort_f = 1;
+            atomicOr(&g_chunk_error, 1);
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity) {
+    for (uint32_t i = 0; i < DRAIN_POLLS && !bar_try(bar, parity); ++i) __nanosleep(128);
+}
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void fence_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+// 32 columns of the thread's TMEM lane, without waiting for them
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+        "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
+        "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+}
+
+template <int HD>
+__device__ __forceinline__ void mma_qk(uint32_t d, uint32_t q, uint32_t k) {
+#pragma unroll
+    for (int kk = 0; kk < HD / 16; ++kk) {
+        const uint32_t off = (kk >> 2) * ATOM + (kk & 3) * 32;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(desc_k(q + off)), "l"(desc_k(k + off)), "r"(IDESC_QK), "r"(kk > 0 ? 1u : 0u)
+            : "memory");
+    }
+}
+// steps of 16 keys: P from TMEM (bf16 pairs, 8 columns a step), V from shared memory
+template <int HD>
+__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t p, uint32_t v, int steps, bool accum) {
+    for (int kk = 0; kk < steps; ++kk)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(p + kk * 8), "l"(desc_mn(v + kk * 2048)), "r"(Geo<HD>::IDESC_PV),
+            "r"((kk > 0 || accum) ? 1u : 0u)
+            : "memory");
+}
+
+// A stretch's part of one item: units [c0, c1) of it; n[t]: units that tile t's rows see any key
+// of, from 0 (none of the rows exist: 0).
+struct Piece {
+    int c0, c1, n[2], kend;
+    __device__ __forceinline__ bool active(int t, int c) const { return c < n[t]; }
+    __device__ __forceinline__ int end(int t) const { return min(c1, n[t]); }
+    __device__ __forceinline__ bool any(int t) const { return c0 < n[t]; }
+    // keys of unit c that the product takes
+    __device__ __forceinline__ int valid(int c) const { return min(UK, kend - c * UK); }
+};
+__device__ __forceinline__ Piece piece_of(const PagedArgs& a, const Line::Cursor& k, long long left) {
+    Piece p;
+    p.c0 = k.unit;
+    p.c1 = (int)min((long long)k.units, k.unit + left);
+    const int row0 = k.tile * RB;
+    p.kend = Line::keys(a, k.q, row0 + RB);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+        p.n[t] = row0 + 128 * t >= k.q.rows ? 0
+                 : k.q.bad                  ? 1
+                                            : (Line::keys(a, k.q, row0 + 128 * (t + 1)) + UK - 1) / UK;
+    return p;
+}
+
+template <int HD>
+__global__ void __launch_bounds__(THREADS, 1)
+    paged_chunk_kernel(const __grid_constant__ CUtensorMap map, PagedArgs a, int box_rows,
+                       PagedDesc* __restrict__ desc, Part<HD>* __restrict__ part) {
+    using G = Geo<HD>;
+    constexpr int STAGES = G::STAGES, TILE = G::TILE;
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    uint8_t* g = raw + (base - smem_u32(raw));
+    const uint32_t ring = base + 2 * TILE;
+    uint8_t* tail = g + (2 + STAGES) * TILE;
+    const uint32_t bar0 = smem_u32(tail);
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    auto q_full = [&](int t) { return bar0 + 8u * (2 * STAGES + t); };
+    auto s_full = [&](int t) { return bar0 + 8u * (2 * STAGES + 2 + t); };
+    auto p_full = [&](int t) { return bar0 + 8u * (2 * STAGES + 4 + t); };
+    auto pv_done = [&](int t) { return bar0 + 8u * (2 * STAGES + 6 + t); };
+    auto o_free = [&](int t) { return bar0 + 8u * (2 * STAGES + 8 + t); };
+    const uint32_t drain = bar0 + 8u * (2 * STAGES + 10);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(tail + 256);
+    volatile int* abort_f = reinterpret_cast<volatile int*>(tail + 260);
+    volatile int* bad_unit = reinterpret_cast<volatile int*>(tail + 264);          // [8]
+    Line::Cursor* first = reinterpret_cast<Line::Cursor*>(tail + 304);
+    static_assert(8 * (2 * STAGES + 11) <= 256 && 304 + sizeof(Line::Cursor) <= G::TAIL, "tail");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            bar_init(full(s), 1);
+            bar_init(empty(s), 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            bar_init(q_full(t), 4);
+            bar_init(s_full(t), 1);
+            bar_init(p_full(t), 4);
+            bar_init(pv_done(t), 1);
+            bar_init(o_free(t), 4);
+        }
+        bar_init(drain, 1);
+        *abort_f = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    grid_dep_launch();                                // the joining kernel may be scheduled
+    // the prefix sums lie in the ring until the stretch is known
+    long long* cum = reinterpret_cast<long long*>(g + 2 * TILE);
+    long long* wsum = cum + GROUPS + 1;
+    const long long L = Line::prefix(a, GROUPS, cum, wsum);
+    const int w = blockIdx.x;
+    const long long stretch = (L + gridDim.x - 1) / gridDim.x;
+    const long long u0 = stretch * w, u1 = min(L, u0 + stretch);
+    if (tid == 0) desc[w].pieces = 0;
+    if (u0 >= u1) return;                             // the whole CTA
+    if (tid == 0) *first = Line::locate(a, GROUPS, cum, u0);
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tslot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_async();                                    // the ring's first use was by plain accesses
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *tslot;
+    auto t_s = [&](int t) { return tmem + (uint32_t)(t * 128); };
+    auto t_o = [&](int t) { return tmem + (uint32_t)(256 + t * 128); };
+    Line::Cursor k = *first;
+
+    int loads = 0;                                    // producer: ring tiles asked for
+    bool issued = false;                              // issuer: any MMA
+    if (warp == 0) {
+        // ---------------- keys and values ----------------
+        const int n_pages = (int)(a.n_slots >> a.page_shift);
+        const int boxes = UK / box_rows;              // row boxes of a tile
+        int unit = 0;
+        bool ok = true;
+        for (long long u = u0; u < u1 && ok;) {
+            const Piece p = piece_of(a, k, u1 - u);
+            const int* table = a.block_table + (size_t)k.r * a.max_blocks;
+            for (int c = p.c0; c < p.c1 && ok; ++c, ++unit) {
+                // lane l of a box row-major list: row box l / NA, column half l % NA
+                const int rb = lane / G::NA, half = lane % G::NA;
+                const int key = c * UK + rb * box_rows;
+                const bool want = rb < boxes && key < p.kend;
+                int row = -1;
+                if (want) {
+                    const int page = table[key >> a.page_shift];
+                    if ((unsigned)page < (unsigned)n_pages)
+                        row = (page << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+                }
+                const unsigned have = __ballot_sync(0xffffffffu, row >= 0);
+                const unsigned asked = __ballot_sync(0xffffffffu, want);
+                const uint32_t bytes = (uint32_t)__popc(have) * (uint32_t)(box_rows * 128);
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const int s = loads % STAGES;
+                    if (!wait_bar(empty(s), ((loads / STAGES) & 1) ^ 1u, abort_f)) { ok = false; break; }
+                    if (lane == 0) {
+                        if (kv == 0) bad_unit[unit & 7] = k.q.bad || have != asked;
+                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full(s)),
+                                     "r"(bytes)
+                                     : "memory");
+                    }
+                    __syncwarp();
+                    if (row >= 0)
+                        asm volatile(
+                            "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                            " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(
+                                ring + (uint32_t)(s * TILE + half * ATOM + rb * box_rows * 128)),
+                            "l"(reinterpret_cast<uint64_t>(&map)), "r"(full(s)), "r"(0), "r"(row),
+                            "r"(k.head * G::NA + half), "r"(kv)
+                            : "memory");
+                    ++loads;
+                }
+            }
+            u += p.c1 - p.c0;
+            Line::advance(a, k, p.c1 - p.c0, u < u1);
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer ----------------
+        if (lane == 0) {
+            // Steps run over the stretch's units; at step i tile t's P V of unit i - 1 comes before
+            // its Q K of unit i.  Q K of a tile waits for the tile's P V before it (P and S share
+            // columns), P V for the softmax.
+            Piece prev, cur;
+            bool have_prev = false, ok = true;
+            int prev_c = 0, unit = 0;                 // unit: ring position of the current one
+            int qi[2] = {0, 0};                       // pieces begun: q_full and o_free phases
+            int si[2] = {0, 0}, pi[2] = {0, 0};       // Q K and P V issued
+            long long u = u0;
+            bool more = true;
+            cur = piece_of(a, k, u1 - u);
+            int c = cur.c0;
+            while (ok) {
+                const int ks = (2 * unit) % STAGES, vs = (2 * unit - 1 + STAGES) % STAGES;
+                if (more && !wait_bar(full(ks), ((2 * unit) / STAGES) & 1, abort_f)) break;
+                if (have_prev && !wait_bar(full(vs), ((2 * unit - 1) / STAGES) & 1, abort_f)) break;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (have_prev && prev.active(t, prev_c)) {
+                        if (!wait_bar(p_full(t), pi[t] & 1, abort_f)) { ok = false; break; }
+                        const bool head = prev_c == prev.c0;
+                        if (head && qi[t] > 1 && !wait_bar(o_free(t), qi[t] & 1, abort_f)) { ok = false; break; }
+                        fence_after();
+                        const int valid = prev.valid(prev_c);
+                        mma_pv<HD>(t_o(t), t_s(t), ring + (uint32_t)(vs * TILE), (valid + 15) / 16, !head);
+                        issued = true;
+                        commit(pv_done(t));
+                        ++pi[t];
+                    }
+                    if (more && cur.active(t, c)) {
+                        if (c == cur.c0) {
+                            if (!wait_bar(q_full(t), qi[t] & 1, abort_f)) { ok = false; break; }
+                            ++qi[t];
+                        }
+                        if (pi[t] > 0 && !wait_bar(pv_done(t), (pi[t] - 1) & 1, abort_f)) { ok = false; break; }
+                        fence_after();
+                        mma_qk<HD>(t_s(t), base + (uint32_t)(t * TILE), ring + (uint32_t)(ks * TILE));
+                        issued = true;
+                        commit(s_full(t));
+                        ++si[t];
+                    }
+                }
+                if (!ok) break;
+                if (have_prev) commit(empty(vs));
+                if (!more) break;
+                commit(empty(ks));
+                have_prev = true;
+                prev = cur;
+                prev_c = c;
+                ++unit;
+                if (++c == cur.c1) {
+                    u += cur.c1 - cur.c0;
+                    more = u < u1;
+                    Line::advance(a, k, cur.c1 - cur.c0, more);
+                    if (more) {
+                        cur = piece_of(a, k, u1 - u);
+                        c = cur.c0;
+                    }
+                }
+            }
+            if (issued) {
+                commit(drain);                        // every MMA retires before TMEM is freed
+                drain_bar(drain, 0);
+            }
+        }
+    } else if (warp >= 4) {
+        // ---------------- softmax and outputs ----------------
+        const int t = (warp - 4) >> 2;
+        const int row = (warp & 3) * 32 + lane;       // row of the tile = TMEM lane
+        const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+        const float sl2 = a.scale * 1.4426950408889634f;
+        uint8_t* qs = g + t * TILE;
+        const uint32_t ts = t_s(t) + lane_addr, to = t_o(t) + lane_addr;
+        auto load_q = [&](const Line::Cursor& at) {
+            const int r = at.tile * RB + t * 128 + row;
+            const bool live = r < at.q.rows;
+            const int rr = live ? r : 0;
+            const uint4* q = reinterpret_cast<const uint4*>(
+                static_cast<const __nv_bfloat16*>(a.q) + (size_t)(at.q.start + rr / a.g) * a.ld_q +
+                (size_t)(at.head * a.g + rr % a.g) * HD);
+#pragma unroll
+            for (int ch = 0; ch < HD / 8; ++ch)
+                *reinterpret_cast<uint4*>(qs + (ch >> 3) * ATOM + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) =
+                    live ? __ldg(q + ch) : make_uint4(0u, 0u, 0u, 0u);
+            fence_async();
+            __syncwarp();
+            if (lane == 0) bar_arrive(q_full(t));
+        };
+        int unit = 0, ns = 0;                         // ring position; S tiles consumed
+        bool ok = true;
+        long long u = u0;
+        Piece p = piece_of(a, k, u1 - u);
+        if (p.any(t)) load_q(k);
+        while (ok) {
+            const Line::Cursor it = k;
+            float m = -FLT_MAX, l[4] = {0.f, 0.f, 0.f, 0.f};
+            bool bad = it.q.bad;
+            const int r = it.tile * RB + t * 128 + row;
+            const bool live = r < it.q.rows;
+            // keys below lim are seen by this row
+            const int lim = it.q.bad || !live ? 0 : it.q.ctx + r / a.g + 1;
+            const int e = p.end(t);
+            for (int c = p.c0; c < e; ++c) {
+                if (!wait_bar(s_full(t), ns & 1, abort_f)) { ok = false; break; }
+                ++ns;
+                fence_after();
+                bad |= bad_unit[(unit + c - p.c0) & 7] != 0;
+                uint32_t sv[128];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) tmem_ld32(ts + j * 32, sv + j * 32);
+                tmem_wait_ld();
+                const int cut = lim - c * UK;
+                if (!__all_sync(0xffffffffu, cut >= UK)) {
+#pragma unroll
+                    for (int j = 0; j < 128; ++j)
+                        if (j >= cut) sv[j] = __float_as_uint(-INFINITY);
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int j = 0; j < 128; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(sv[j]));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+                // the reference moves when the maximum is over 2^8 above it (at first, at once)
+                const bool move = top > m + 8.f;
+                if (__any_sync(0xffffffffu, move)) {
+                    const float mn = move ? top : m;
+                    const float f = ex2(m - mn);      // 1 where it stays; 0 from the start value
+                    if (c > p.c0) {
+                        // the tile's P V before this unit has retired: this S waited for it
+#pragma unroll 1
+                        for (int j = 0; j < HD / 32; ++j) {
+                            uint32_t v[32];
+                            tmem_ld32(to + j * 32, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+                            tmem_st32(to + j * 32, v);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) l[i] *= f;
+                    m = mn;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int j = 0; j < 64; j += 2) {
+                        const float p0 = ex2(fmaf(__uint_as_float(sv[h * 64 + j]), sl2, -m));
+                        const float p1 = ex2(fmaf(__uint_as_float(sv[h * 64 + j + 1]), sl2, -m));
+                        l[j & 3] += p0;
+                        l[(j + 1) & 3] += p1;
+                        pk[j / 2] = pack2(p0, p1);
+                    }
+                    tmem_st32(ts + h * 32, pk);
+                }
+                tmem_wait_st();
+                const int valid = p.valid(c);
+                if (valid < UK && (valid & 15)) {
+                    // the value rows behind the last key, up to the end of its 16-key step
+                    const int vt = 2 * (unit + c - p.c0) + 1, vs = vt % STAGES;
+                    if (!wait_bar(full(vs), (vt / STAGES) & 1, abort_f)) { ok = false; break; }
+                    const int rows = 16 - (valid & 15);
+                    for (int i = (warp & 3) * 32 + lane; i < rows * (HD / 8); i += 128) {
+                        const int vr = valid + i / (HD / 8), ch = i % (HD / 8);
+                        *reinterpret_cast<uint4*>(g + (2 + vs) * TILE + (ch >> 3) * ATOM + vr * 128 +
+                                                  ((ch & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_async();
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(p_full(t));
+            }
+            if (!ok) break;
+            unit += p.c1 - p.c0;
+            u += p.c1 - p.c0;
+            const bool more = u < u1;
+            const Piece done = p;
+            Line::advance(a, k, p.c1 - p.c0, more);
+            if (more) {
+                // the next piece's rows: every Q K of this one has retired (its last S was read)
+                p = piece_of(a, k, u1 - u);
+                if (p.any(t)) load_q(k);
+            }
+            const bool whole = done.c0 == 0 && done.c1 == it.units;
+            const float lt = bad ? __int_as_float(0x7fc00000) : (l[0] + l[1]) + (l[2] + l[3]);
+            Part<HD>* slot = part + 2 * w + (done.c0 == 0 ? 1 : 0);
+            if (!whole) {
+                slot->m[t * 128 + row] = m;
+                slot->l[t * 128 + row] = lt;
+                if (t == 0 && row == 0 && done.c0 == 0) {
+                    const long long last = u - (done.c1 - done.c0) + it.units - 1;
+                    PagedDesc d;
+                    d.pieces = (int)(last / stretch) - w + 1;
+                    d.start = it.q.start;
+                    d.row0 = it.tile * RB;
+                    d.rows = min(RB, it.q.rows - it.tile * RB);
+                    d.kvh = it.head;
+                    desc[w] = d;
+                }
+            }
+            if (done.any(t)) {
+                if (!wait_bar(pv_done(t), (ns - 1) & 1, abort_f)) { ok = false; break; }
+                fence_after();
+                const float inv = 1.f / lt;
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                                     (size_t)(it.q.start + r / a.g) * a.ld_out +
+                                     (size_t)(it.head * a.g + r % a.g) * HD;
+#pragma unroll 1
+                for (int j = 0; j < HD / 32; ++j) {
+                    uint32_t v[32];
+                    tmem_ld32(to + j * 32, v);
+                    tmem_wait_ld();
+                    if (live && whole) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            auto pr = [&](int x) {
+                                return pack2(__uint_as_float(v[8 * i + 2 * x]) * inv,
+                                             __uint_as_float(v[8 * i + 2 * x + 1]) * inv);
+                            };
+                            *reinterpret_cast<uint4*>(out + j * 32 + i * 8) = make_uint4(pr(0), pr(1), pr(2), pr(3));
+                        }
+                    } else if (live) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            slot->o[j * 8 + i][t * 128 + row] =
+                                make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                            __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+                    }
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(o_free(t));
+            }
+            if (!more) break;
+        }
+    }
+    __syncthreads();                                  // every role has left its loop
+    if (*abort_f && warp == 0 && lane == 0)
+        for (int i = loads - 1; i >= 0 && i >= loads - STAGES; --i)
+            drain_bar(full(i % STAGES), (i / STAGES) & 1);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// Adds the pieces of the item that worker blockIdx.x's stretch ended inside, in key order: one row
+// per thread; a piece whose keys a row does not see has l = 0 and no output.
+constexpr int JOIN_ROWS = 32, JOIN_THREADS = 256;
+template <int HD>
+__global__ void __launch_bounds__(JOIN_THREADS)
+    paged_chunk_join_kernel(PagedArgs a, const PagedDesc* __restrict__ desc, const Part<HD>* __restrict__ part) {
+    grid_dep_wait();
+    const int w = blockIdx.x;
+    const PagedDesc d = desc[w];
+    const int row = blockIdx.y * JOIN_ROWS + (threadIdx.x & 31), dg = threadIdx.x >> 5;
+    if (d.pieces <= 0 || row >= d.rows) return;
+    auto piece = [&](int i) -> const Part<HD>& { return part[2 * (w + i) + (i == 0 ? 1 : 0)]; };
+    float m = -FLT_MAX, l = 0.f;
+    for (int i = 0; i < d.pieces; ++i) m = fmaxf(m, piece(i).m[row]);
+    constexpr int DG = HD / 4 / (JOIN_THREADS / 32);  // float4 groups of a thread
+    float4 o[DG];
+#pragma unroll
+    for (int j = 0; j < DG; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < d.pieces; ++i) {
+        const Part<HD>& p = piece(i);
+        const float li = p.l[row];
+        if (li == 0.f) continue;
+        const float f = ex2(p.m[row] - m);
+        l = fmaf(f, li, l);
+#pragma unroll
+        for (int j = 0; j < DG; ++j) {
+            const float4 v = p.o[dg * DG + j][row];
+            o[j].x = fmaf(f, v.x, o[j].x);
+            o[j].y = fmaf(f, v.y, o[j].y);
+            o[j].z = fmaf(f, v.z, o[j].z);
+            o[j].w = fmaf(f, v.w, o[j].w);
+        }
+    }
+    const float inv = 1.f / l;
+    const int q = d.row0 + row;
+    uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) +
+                                          (size_t)(d.start + q / a.g) * a.ld_out +
+                                          (size_t)(d.kvh * a.g + q % a.g) * HD) + dg * DG;
+#pragma unroll
+    for (int j = 0; j < DG; ++j)
+        out[j] = make_uint2(pack2(o[j].x * inv, o[j].y * inv), pack2(o[j].z * inv, o[j].w * inv));
+}
+
+template <int HD>
+cudaError_t launch_chunk(const PagedArgs& a, cudaStream_t st) {
+    CUtensorMap map;
+    const int box_rows = min(UK, 1 << a.page_shift);
+    if (!paged_cache_map(&map, a, box_rows, 1, 1)) return cudaErrorNotSupported;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(paged_chunk_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Geo<HD>::SMEM);
+    if (e != cudaSuccess) return e;
+    const int grid = min(sms, MAX_CTAS);
+    PagedDesc* desc = static_cast<PagedDesc*>(a.ws);
+    auto* part = reinterpret_cast<Part<HD>*>(static_cast<char*>(a.ws) + MAX_CTAS * sizeof(PagedDesc));
+    paged_chunk_kernel<HD><<<grid, THREADS, Geo<HD>::SMEM, st>>>(map, a, box_rows, desc, part);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_pdl(paged_chunk_join_kernel<HD>, dim3(grid, RB / JOIN_ROWS), dim3(JOIN_THREADS), 0, st, a,
+                      static_cast<const PagedDesc*>(desc), static_cast<const Part<HD>*>(part));
+}
+
+}  // namespace
+
+size_t paged_chunk_workspace(int hd) {
+    const size_t p = hd == 128 ? sizeof(Part<128>) : sizeof(Part<64>);
+    return MAX_CTAS * (sizeof(PagedDesc) + 2 * p);
+}
+
+cudaError_t launch_paged_chunk(const PagedArgs& a, cudaStream_t st) {
+    if (a.n_tokens <= 0 || a.n_rows <= 0) return cudaSuccess;
+    return a.hd == 128 ? launch_chunk<128>(a, st) : launch_chunk<64>(a, st);
+}
+
+int paged_chunk_error_word() {
+    int v = 0;
+    const int zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_chunk_error, sizeof(int)) != cudaSuccess) return -1;
+    cudaMemcpyToSymbol(g_chunk_error, &zero, sizeof(int));
+    return v;
+}
+
+}  // namespace zo

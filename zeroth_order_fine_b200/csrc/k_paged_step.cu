@@ -22,11 +22,9 @@
 //   the packed attention does (the sum l is of the unrounded values).
 // Keys a query may not see get probability exactly 0; value rows behind the tile's last key are
 // cleared in registers (0 x NaN would not be 0).
-#include <cuda.h>
 #include <float.h>
 
-#include "common.cuh"
-#include "kernels.h"
+#include "paged.cuh"
 
 namespace zo {
 
@@ -107,78 +105,9 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// What this kernel takes of request r: its rows per kv head (new tokens x g), 0 when it is left
-// out or has none, and whether its length can be used.
-struct Req {
-    int start, rows, ctx;
-    bool bad;
-};
-__device__ __forceinline__ Req get_req(const PagedArgs& a, int r) {
-    Req q;
-    const int s = a.cu_new[r], e = a.cu_new[r + 1], len = a.lens[r];
-    const int n = e - s;
-    const bool in = s >= 0 && e >= s && e <= a.n_tokens;
-    q.start = s;
-    q.rows = in && n <= a.step_tokens ? n * a.g : 0;
-    q.bad = len < n || (long long)len > ((long long)a.max_blocks << a.page_shift);
-    q.ctx = len - n;
-    return q;
-}
-// Keys (the end) and units of tile t of a request's rows, RB rows to a tile.
-template <int RB>
-__device__ __forceinline__ int tile_keys(const PagedArgs& a, const Req& q, int t) {
-    return q.ctx + (min((t + 1) * RB, q.rows) - 1) / a.g + 1;
-}
-template <int RB>
-__device__ __forceinline__ int tile_units(const PagedArgs& a, const Req& q, int t) {
-    return q.bad ? 1 : (tile_keys<RB>(a, q, t) + UK - 1) / UK;
-}
-template <int RB>
-__device__ __forceinline__ long long req_units(const PagedArgs& a, int r) {
-    const Req q = get_req(a, r);
-    long long u = 0;
-    for (int t = 0; t * RB < q.rows; ++t) u += tile_units<RB>(a, q, t);
-    return u * a.Hkv;
-}
-
-// A place on the line of units.
-struct Cursor {
-    Req q;
-    int r, tile, head, unit, units;
-};
-// The next request from r on that has rows here (there is one: the stretch is not used up).
-__device__ __forceinline__ void seek_req(const PagedArgs& a, Cursor& c) {
-    c.q.rows = 0;
-    while (c.r < a.n_rows) {
-        c.q = get_req(a, c.r);
-        if (c.q.rows > 0) return;
-        ++c.r;
-    }
-}
-// To the next unit; `more`: the stretch goes on behind it.
-template <int RB>
-__device__ __forceinline__ void advance(const PagedArgs& a, Cursor& c, bool more) {
-    if (++c.unit < c.units) return;
-    c.unit = 0;
-    if (++c.head < a.Hkv) return;
-    c.head = 0;
-    if (!more) return;
-    if (++c.tile * RB >= c.q.rows) {
-        c.tile = 0;
-        ++c.r;
-        seek_req(a, c);
-    }
-    c.units = tile_units<RB>(a, c.q, c.tile);
-}
-
 // Slots of partial results, in the accumulator's own layout: slot 2 w: the piece with which worker
 // w's stretch begins (an item begun by an earlier worker); 2 w + 1: the one it ends with (an item
 // that goes on).  desc[w] describes the item of slot 2 w + 1.
-struct Desc {
-    int pieces;                       // workers w .. w + pieces - 1 hold a piece; 0: none
-    int start, row0, rows;            // first packed row; first and number of the request's rows
-    int kvh, pad[3];
-};
 template <int HD, int NB>
 struct Part {
     float4 o[HD / 16][NB][32];
@@ -209,7 +138,7 @@ __device__ __forceinline__ void store_rows(const PagedArgs& a, int start, int ro
 template <int HD, int NB>
 __global__ void __launch_bounds__(THREADS, 1)
     paged_step_kernel(const __grid_constant__ CUtensorMap map, PagedArgs a, int box_rows,
-                      Desc* __restrict__ desc, Part<HD, NB>* __restrict__ part) {
+                      PagedDesc* __restrict__ desc, Part<HD, NB>* __restrict__ part) {
     using G = Geo<HD>;
     constexpr int RB = NB * 8, NH = G::NH, STAGES = G::STAGES;
     extern __shared__ uint8_t raw[];
@@ -225,69 +154,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     grid_dep_launch();                                // the joining kernel may be scheduled
 
-    // prefix sums of the requests' units, in groups of c requests
-    const int c = (a.n_rows + GROUPS - 1) / GROUPS;
-    const int groups = (a.n_rows + c - 1) / c;
-    long long base = 0;
-    for (int g0 = 0; g0 < groups; g0 += THREADS) {
-        const int gi = g0 + tid;
-        long long u = 0;
-        if (gi < groups)
-            for (int r = gi * c; r < min(a.n_rows, (gi + 1) * c); ++r) u += req_units<RB>(a, r);
-        long long incl = u;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        if (lane == 31) wsum[warp] = incl;
-        __syncthreads();
-        long long before = 0, total = 0;
-        for (int w = 0; w < WARPS; ++w) {
-            if (w < warp) before += wsum[w];
-            total += wsum[w];
-        }
-        if (gi < groups) cum[gi + 1] = base + before + incl;
-        base += total;
-        __syncthreads();
-    }
-    if (tid == 0) cum[0] = 0;
-    __syncthreads();
-    const long long L = base;
+    using Line = PagedLine<false, RB, UK>;
+    const long long L = Line::prefix(a, GROUPS, cum, wsum);
     const int workers = gridDim.x * WARPS, w = blockIdx.x * WARPS + warp;
     const long long stretch = (L + workers - 1) / workers;      // units per worker
     const long long u0 = stretch * w, u1 = min(L, u0 + stretch);
     if (lane == 0) desc[w].pieces = 0;
     if (u0 >= u1) return;                             // nothing to do, nothing in flight
 
-    Cursor con;
-    {
-        int lo = 0, hi = groups;                      // the last group with cum <= u0
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (cum[mid] <= u0) lo = mid;
-            else hi = mid;
-        }
-        long long rest = u0 - cum[lo];
-        con.r = lo * c;
-        for (;; ++con.r) {                            // within the group
-            const long long u = c == 1 ? LLONG_MAX : req_units<RB>(a, con.r);
-            if (rest < u) break;
-            rest -= u;
-        }
-        con.q = get_req(a, con.r);
-        con.tile = 0;
-        for (;;) {
-            con.units = tile_units<RB>(a, con.q, con.tile);
-            const long long u = (long long)con.units * a.Hkv;
-            if (rest < u) break;
-            rest -= u;
-            ++con.tile;
-        }
-        con.head = (int)(rest / con.units);
-        con.unit = (int)(rest % con.units);
-    }
-    Cursor pro = con;
+    typename Line::Cursor con = Line::locate(a, GROUPS, cum, u0);
+    typename Line::Cursor pro = con;
 
     // ---- producer side of the warp: unit `pro` into stage ps ----
     const int n_pages = (int)(a.n_slots >> a.page_shift);
@@ -308,7 +184,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         int row[2] = {-1, -1};
         bool bad = pro.q.bad;
         if (!bad) {
-            const int kend = tile_keys<RB>(a, pro.q, pro.tile);
+            const int kend = Line::keys(a, pro.q, (pro.tile + 1) * RB);
             const int subs = UK / box_rows;           // boxes per unit: 1, or 2 with pages of 8
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -343,7 +219,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int s = 0; s < STAGES && issued < u1; ++s) {
         issue(s);
         ++issued;
-        advance<RB>(a, pro, issued < u1);
+        Line::advance(a, pro, 1, issued < u1);
     }
 
     // ---- consumer side ----
@@ -368,7 +244,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             fresh = false;
             first_unit = con.unit;
             bad = con.q.bad;
-            kend = con.q.bad ? 0 : tile_keys<RB>(a, con.q, con.tile);
+            kend = Line::keys(a, con.q, (con.tile + 1) * RB);
             const int row0 = con.tile * RB;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
@@ -476,7 +352,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (issued < u1) {
             issue(stage);
             ++issued;
-            advance<RB>(a, pro, issued < u1);
+            Line::advance(a, pro, 1, issued < u1);
         }
         if (++stage == STAGES) {
             stage = 0;
@@ -520,7 +396,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (first_unit == 0 && lane == 0) {
                     // the item's last unit is (units - 1) behind its first, which is u - unit
                     const long long last = u - con.unit + con.units - 1;
-                    Desc d;
+                    PagedDesc d;
                     d.pieces = (int)(last / stretch) - w + 1;
                     d.start = con.q.start;
                     d.row0 = row0;
@@ -530,7 +406,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
         }
-        advance<RB>(a, con, u + 1 < u1);
+        Line::advance(a, con, 1, u + 1 < u1);
     }
     if (!alive) {
         // the copies still in flight land (or the bound ends) before the memory goes away
@@ -546,13 +422,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 // Adds the pieces of the item that worker w's stretch ended inside, in key order: one warp per
 // worker, in the partials' own layout.
 template <int HD, int NB>
-__global__ void __launch_bounds__(128) paged_step_join_kernel(PagedArgs a, const Desc* __restrict__ desc,
+__global__ void __launch_bounds__(128) paged_step_join_kernel(PagedArgs a, const PagedDesc* __restrict__ desc,
                                                               const Part<HD, NB>* __restrict__ part,
                                                               int workers) {
     grid_dep_wait();
     const int w = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (w >= workers) return;
-    const Desc d = desc[w];
+    const PagedDesc d = desc[w];
     if (d.pieces <= 0) return;
     const float sl2 = a.scale * 1.4426950408889634f;
     float o[HD / 16][NB][4], m[NB][2], l[NB][2];
@@ -606,42 +482,11 @@ __global__ void __launch_bounds__(128) paged_step_join_kernel(PagedArgs a, const
     store_rows<HD, NB>(a, d.start, d.row0, d.rows, d.kvh, o, inv, lane);
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_fn() {
-    static const EncodeTiledFn fn = []() -> EncodeTiledFn {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            return reinterpret_cast<EncodeTiledFn>(p);
-        return nullptr;
-    }();
-    return fn;
-}
-
-// The cache [n_slots][2][Hkv][HD] as (64 columns, rows, column halves of all heads, k/v): a box of
-// 64 x rows x HD/64 x 2 is one head's keys and values of `rows` consecutive cache rows.
-bool cache_map(CUtensorMap* m, const PagedArgs& a, int rows) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t kv = (cuuint64_t)a.Hkv * a.hd * 2;          // bytes of a row's keys
-    const cuuint64_t dims[4] = {64, (cuuint64_t)a.n_slots, (cuuint64_t)(a.Hkv * a.hd / 64), 2};
-    const cuuint64_t strides[3] = {2 * kv, 128, kv};
-    const cuuint32_t box[4] = {64, (cuuint32_t)rows, (cuuint32_t)(a.hd / 64), 2};
-    const cuuint32_t es[4] = {1, 1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.cache), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int HD, int NB>
 cudaError_t launch_step(const PagedArgs& a, cudaStream_t st) {
     CUtensorMap map;
     const int box_rows = min(UK, 1 << a.page_shift);
-    if (!cache_map(&map, a, box_rows)) return cudaErrorNotSupported;
+    if (!paged_cache_map(&map, a, box_rows, HD / 64, 2)) return cudaErrorNotSupported;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -650,21 +495,21 @@ cudaError_t launch_step(const PagedArgs& a, cudaStream_t st) {
                                  Geo<HD>::SMEM);
     if (e != cudaSuccess) return e;
     const int grid = min(sms, MAX_CTAS);
-    Desc* desc = static_cast<Desc*>(a.ws);
-    auto* part = reinterpret_cast<Part<HD, NB>*>(static_cast<char*>(a.ws) + MAX_WORKERS * sizeof(Desc));
+    PagedDesc* desc = static_cast<PagedDesc*>(a.ws);
+    auto* part = reinterpret_cast<Part<HD, NB>*>(static_cast<char*>(a.ws) + MAX_WORKERS * sizeof(PagedDesc));
     paged_step_kernel<HD, NB><<<grid, THREADS, Geo<HD>::SMEM, st>>>(map, a, box_rows, desc, part);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int workers = grid * WARPS;
     return launch_pdl(paged_step_join_kernel<HD, NB>, dim3((workers + 3) / 4), dim3(128), 0, st, a,
-                      static_cast<const Desc*>(desc), static_cast<const Part<HD, NB>*>(part), workers);
+                      static_cast<const PagedDesc*>(desc), static_cast<const Part<HD, NB>*>(part), workers);
 }
 
 }  // namespace
 
 size_t paged_step_workspace(int hd) {
     const size_t p = hd == 128 ? sizeof(Part<128, 2>) : sizeof(Part<64, 2>);
-    return MAX_WORKERS * (sizeof(Desc) + 2 * p);
+    return MAX_WORKERS * (sizeof(PagedDesc) + 2 * p);
 }
 
 bool paged_tc_supported(const PagedArgs& a) {

@@ -206,6 +206,9 @@ bool paged_tc_supported(const PagedArgs& a);                               // bf
 cudaError_t launch_paged_step(const PagedArgs& a, cudaStream_t st);
 size_t paged_step_workspace(int hd);
 int paged_step_error_word();
+cudaError_t launch_paged_chunk(const PagedArgs& a, cudaStream_t st);       // the other requests
+size_t paged_chunk_workspace(int hd);
+int paged_chunk_error_word();
 
 // ---- serving: one adapter per row ----------------------------------------------------------
 struct AdapterArgs {

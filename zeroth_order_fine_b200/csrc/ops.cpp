@@ -329,7 +329,7 @@ size_t zo_op_attention_paged_workspace(int32_t n_tokens, int32_t n_rows, int32_t
                                        int32_t n_kv_heads, int32_t head_dim, int32_t dtype) {
     (void)n_tokens; (void)n_rows; (void)n_heads; (void)n_kv_heads;
     if (dtype != ZO_DTYPE_BF16 || (head_dim != 64 && head_dim != 128)) return 256;
-    return paged_step_workspace(head_dim);
+    return std::max(paged_step_workspace(head_dim), paged_chunk_workspace(head_dim));
 }
 
 int zo_op_attention_paged(const void* q, int64_t ld_q, const void* cache, int64_t n_slots,
@@ -347,7 +347,7 @@ int zo_op_attention_paged(const void* q, int64_t ld_q, const void* cache, int64_
     if (n_slots < page_size || n_slots % page_size || n_slots > 0x7fffffffLL) return ZO_ERR_ARG;
     if (head_dim != 32 && head_dim != 64 && head_dim != 128 && head_dim != 256)
         return ZO_ERR_UNSUPPORTED;
-    if (n_kv_heads > 65535 || (int64_t)n_tokens * (n_heads / n_kv_heads) > 0x7fffffffLL)
+    if (n_kv_heads > 65535 || (int64_t)n_tokens * (n_heads / n_kv_heads) > (1 << 30))
         return ZO_ERR_UNSUPPORTED;
     if (n_rows == 0 || n_tokens == 0) return ZO_OK;
     if (!q || !cache || !block_table || !cu_new || !lens || !out) return ZO_ERR_ARG;
@@ -366,10 +366,15 @@ int zo_op_attention_paged(const void* q, int64_t ld_q, const void* cache, int64_
     a.dtype = dtype == ZO_DTYPE_BF16 ? E_BF16 : E_F32;
     a.out = out; a.ld_out = ld_out;
     a.ws = ws;
-    a.step_tokens = 0x7fffffff;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (impl != ZO_IMPL_CUDA_CORES && paged_tc_supported(a)) {
-        if (launch_paged_step(a, st) != cudaSuccess) return op_fail("paged attention launch failed");
+        // up to 16 query rows per kv head: the decode-step kernel; more: the chunk kernel
+        const bool chunks = (int64_t)max_new * a.g > 16;
+        a.step_tokens = chunks ? 16 / a.g : 0x7fffffff;
+        if (a.step_tokens > 0 && launch_paged_step(a, st) != cudaSuccess)
+            return op_fail("paged attention launch failed");
+        if (chunks && launch_paged_chunk(a, st) != cudaSuccess)
+            return op_fail("paged attention launch failed");
         return ZO_OK;
     }
     if (impl == ZO_IMPL_TENSOR_CORES) return ZO_ERR_UNSUPPORTED;
@@ -426,8 +431,9 @@ int zo_op_error_word(void) {
     const int v = gemm_tc_error_word();
     const int w = attention_tc_error_word();
     const int s = paged_step_error_word();
-    if (v < 0 || w < 0 || s < 0) return -1;
-    return v | w | s;
+    const int c = paged_chunk_error_word();
+    if (v < 0 || w < 0 || s < 0 || c < 0) return -1;
+    return v | w | s | c;
 }
 
 int zo_debug_build(void) {
