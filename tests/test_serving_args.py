@@ -125,9 +125,11 @@ def test_linear_adapters_of_no_rows_is_a_no_op(L):
 
 def test_workspace_sizes(L):
     assert zo.zo_op_attention_paged_workspace(1, 1, 32, 8, 128) > 0
-    assert zo.zo_op_linear_adapters_workspace(1, 256, 128, 4, 16) > 0
-    big = zo.zo_op_linear_adapters_workspace(4096, 5120, 5120, 32, 64)
-    assert big >= zo.zo_op_linear_adapters_workspace(64, 5120, 5120, 32, 64)
+    for M in (1, 128, 129, 4096):
+        # the rows' shrink at least, whatever form they take
+        assert zo.zo_op_linear_adapters_workspace(M, 256, 128, 4, 16) >= M * 16 * 4
+        assert zo.zo_op_linear_adapters_workspace(M, 256, 128, 4, 16, torch.float32) >= M * 16 * 4
+    assert zo.zo_op_linear_adapters_workspace(-1, 256, 128, 4, 16) == 0
 
 
 def test_binding_refuses_host_tensors():

@@ -100,6 +100,14 @@ struct TcParams {
     int ksplit, kbs;                        // split-K (SPLIT kernels): splits, main blocks each
     int* err;
     long long wait_cycles;                  // bound of every mbarrier wait (clock64 cycles)
+    int dep_late;                           // EPI_SPLIT_T: wait for the kernel before at the end
+    // adapters (LIST kernels): row block mb takes cnt[mb] extension blocks, list[mb * n_list + i]
+    // = block | mask of its 16-column steps << 16; odd[m / 32][n / 32]: a chunk whose accumulators
+    // are not all finite (left to the repair kernel)
+    const int* cnt; const int* list; int n_list;
+    uint8_t* odd;
+    // the adapters' shrink: row ids, scales, rank
+    const int* ids; const float* ad_scale; int n_adapters, ad_rank;
 };
 
 // ---- PTX wrappers ------------------------------------------------------------------
@@ -410,8 +418,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     constexpr int STAGE_BYTES = T1::STAGE_BYTES;
     if (EPI == EPI_SPLIT_T) {
         // launched as a dependent of the kernel that wrote its operands; its split reduction
-        // is launched as a dependent of this one
-        grid_dep_wait();
+        // is launched as a dependent of this one (dep_late: the kernel before wrote only what
+        // the reduction reads, so it is waited for at the end)
+        if (!p.dep_late) grid_dep_wait();
         grid_dep_launch();
     }
     extern __shared__ uint8_t smem_raw[];
@@ -629,6 +638,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                      "r"(T1::TMEM_COLS)
                      : "memory");
     }
+    if (EPI == EPI_SPLIT_T && p.dep_late) grid_dep_wait();
 }
 
 // ---- 2-SM variant ----------------------------------------------------------------
@@ -770,16 +780,36 @@ __device__ __forceinline__ void dequant_chunk(const TcParams& p, int m, int n, f
     }
 }
 
+template <int W>
+__device__ __forceinline__ float zero_times(const float* v) {
+    float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < W; ++j) z[j & 3] = fmaf(v[j], 0.f, z[j & 3]);
+    return (z[0] + z[1]) + (z[2] + z[3]);
+}
+
 // Pair-kernel epilogue: each warp stages its 32 rows x (32 fp32 | 64 bf16) columns in
 // shared memory and one lane hands them to the TMA unit -- a store, or for the
 // residual stream an fp32 reduce-add, so the SM never reads the residual.  Two
 // staging buffers per warp alternate; a buffer is rewritten only after the TMA
 // has read it.
-template <int EPI, bool F8, bool SPLIT>
+//
+// LIST (adapters): a row's extension columns of other adapters are 0, and 0 times a non-finite
+// expand factor would not be 0.  So a chunk of 32 columns with an accumulator that is not finite
+// is not stored but marked, and the repair kernel computes it from the rows' own factors.
+template <int EPI, bool F8, bool SPLIT, bool LIST>
 __device__ __forceinline__ void epilogue_tma(const TcParams& p, const CUtensorMap* tmC,
                                              uint32_t stg, uint8_t* stg_ptr, int& buf, int m_base,
                                              int nb, uint32_t taddr, int lane, int split) {
     const int r = lane;
+    // marks the 32-column chunks from column n (z: the sum of 0 times the thread's accumulators,
+    // NaN if one is not finite); true: not to be stored
+    auto is_odd = [&](float z, int n, int chunks) {
+        const bool odd = __any_sync(0xffffffffu, z != 0.f);
+        if (lane < chunks && n + 32 * lane < p.N && m_base < p.M)
+            p.odd[(size_t)(m_base >> 5) * ((p.N + 31) >> 5) + (n >> 5) + lane] = odd;
+        return odd;
+    };
     auto stage_begin = [&]() {
         if (lane == 0) bulk_wait_read1();
         __syncwarp();
@@ -822,6 +852,7 @@ __device__ __forceinline__ void epilogue_tma(const TcParams& p, const CUtensorMa
             if (n >= p.N) break;
             float v[32];
             tmem_ld32(taddr + (uint32_t)(c * 32), v);
+            if (LIST && is_odd(zero_times<32>(v), n, 1)) continue;
             if (p.bias) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] += (n + j < p.N) ? __ldg(p.bias + n + j) : 0.f;
@@ -962,6 +993,7 @@ __device__ __forceinline__ void epilogue_tma(const TcParams& p, const CUtensorMa
             tmem_ld32(taddr + (uint32_t)(c * 32), y);
             tmem_ld32(taddr + (uint32_t)((c + 1) * 32), y + 32);
             if (F8) dequant_chunk<64>(p, m_base + r, n, y);
+            if (LIST && is_odd(zero_times<64>(y), n, 2)) continue;
 #pragma unroll
             for (int j = 0; j < 64; ++j) {
                 float v = y[j];
@@ -992,8 +1024,9 @@ __device__ __forceinline__ void tile_coords2(int t, const TcParams& p, int* mb, 
 }
 
 // F8: the main K blocks are E4M3 (kind::f8f6f4) and the epilogue dequantises; a separate
-// instantiation, so the bf16 kernels carry none of it.
-template <int EPI, bool F8, bool SPLIT>
+// instantiation, so the bf16 kernels carry none of it.  LIST (adapters): a row block takes only
+// the extension blocks on its list, and of each block only the 16-column steps in its mask.
+template <int EPI, bool F8, bool SPLIT, bool LIST>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     gemm_tc2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmA2,
@@ -1046,11 +1079,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     // work items: tiles, or (tile, K split) pairs; a split takes kbs main K blocks and the
     // last split also the extension blocks
     const int n_items = SPLIT ? p.n_tiles * p.ksplit : p.n_tiles;
-    auto item_blocks = [&](int sp, int* kb0, int* n_main, int* n_kb) {
+    auto item_blocks = [&](int mb, int sp, int* kb0, int* n_main, int* n_kb) {
         if (!SPLIT) {
             *kb0 = 0;
             *n_main = p.kb_main;
-            *n_kb = p.kb_main + p.kb_ext;
+            *n_kb = p.kb_main + (LIST ? p.cnt[mb] : p.kb_ext);
             return;
         }
         *kb0 = sp * p.kbs;
@@ -1072,9 +1105,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                 const int row_a = mb * BM2 + (int)rank * 128;
                 const int row_b = nb * BN + (int)rank * 128;
                 int kb0, n_main, n_kb;
-                item_blocks(SPLIT ? t % p.ksplit : 0, &kb0, &n_main, &n_kb);
+                item_blocks(mb, SPLIT ? t % p.ksplit : 0, &kb0, &n_main, &n_kb);
                 for (int i = 0; i < n_kb; ++i) {
-                    const int kb = i < n_main ? kb0 + i : p.kb_main + (i - n_main);
+                    int kb = i < n_main ? kb0 + i : p.kb_main + (i - n_main);
+                    if (LIST && i >= n_main)
+                        kb = p.kb_main + (p.list[(size_t)mb * p.n_list + (i - n_main)] & 0xFFFF);
                     if (!mbar_wait(empty(s), ph ^ 1u, abort_f, p.err, p.wait_cycles)) { ok = false; break; }
                     const uint32_t sa = base + s * STAGE2_BYTES;
                     const uint32_t sb = sa + A2B;
@@ -1106,10 +1141,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                 if (!mbar_wait(tempty(acc), aph ^ 1u, abort_f, p.err, p.wait_cycles)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(acc * BN);
+                int mb = 0, nb = 0;
+                if (LIST) tile_coords2(t, p, &mb, &nb);
                 int kb0, n_main, n_kb;
-                item_blocks(SPLIT ? t % p.ksplit : 0, &kb0, &n_main, &n_kb);
+                item_blocks(mb, SPLIT ? t % p.ksplit : 0, &kb0, &n_main, &n_kb);
                 for (int i = 0; i < n_kb; ++i) {
                     const int kb = i < n_main ? kb0 + i : p.kb_main + (i - n_main);
+                    const int steps = LIST && i >= n_main
+                                          ? p.list[(size_t)mb * p.n_list + (i - n_main)] >> 16 : 0xF;
                     if (!mbar_wait(full(s), ph, abort_f, p.err, p.wait_cycles)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t sa = base + s * STAGE2_BYTES;
@@ -1122,8 +1161,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                     } else {
 #pragma unroll
                         for (int kk = 0; kk < BK / 16; ++kk)
-                            tc_mma_pair(d, sw128_desc(sa + kk * 32), sw128_desc(sb + kk * 32),
-                                        kIdesc2, (i > 0 || kk > 0) ? 1u : 0u);
+                            if (!LIST || ((steps >> kk) & 1))
+                                tc_mma_pair(d, sw128_desc(sa + kk * 32), sw128_desc(sb + kk * 32),
+                                            kIdesc2, (i > 0 || kk > 0) ? 1u : 0u);
                     }
                     issued = true;
                     tc_commit_pair(empty(s));       // stage free in both CTAs
@@ -1150,7 +1190,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             if (!mbar_wait(tfull(acc), aph, abort_f, p.err, p.wait_cycles)) break;
             tc_fence_after();
             const int m_base = mb * BM2 + (int)rank * 128 + lane_base;
-            epilogue_tma<EPI, F8, SPLIT>(p, &tmC, stg, stg_ptr, buf, m_base, nb,
+            epilogue_tma<EPI, F8, SPLIT, LIST>(p, &tmC, stg, stg_ptr, buf, m_base, nb,
                                          tmem + ((uint32_t)lane_base << 16) + (uint32_t)(acc * BN),
                                          lane, SPLIT ? t % p.ksplit : 0);
             tc_fence_before();
@@ -1251,7 +1291,12 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, f
                  : "memory");
 }
 
-template <int BNT>
+//
+// LIST (adapters, BNT 128): an item is a 128-row tile and two of its row block's listed 64-row
+// blocks of the factors; a row keeps the columns of its own adapter, times the adapter's scale,
+// and has zeros in the others.
+constexpr int MAX_LIST_BLOCKS = 1024;        // 256-row blocks of one LIST launch
+template <int BNT, bool LIST>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     shrink_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                        const __grid_constant__ CUtensorMap tmB, const TcParams p) {
@@ -1276,6 +1321,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + TS::SLOT_OFF);
     volatile int* abort_f = reinterpret_cast<volatile int*>(tail + TS::ABORT_OFF);
 
+    __shared__ int cum[LIST ? MAX_LIST_BLOCKS + 1 : 1];   // items before each 256-row block
+    if constexpr (LIST) {
+        grid_dep_wait();                     // the lists
+        if (threadIdx.x < 32) {
+            int base = 0;
+            const int lane = threadIdx.x;
+            for (int b0 = 0; b0 < p.n_m_blk; b0 += 32) {
+                // both halves of a row block take its blocks, two at a time
+                const int c = b0 + lane < p.n_m_blk ? 2 * ((p.cnt[b0 + lane] + 1) / 2) : 0;
+                int incl = c;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += v;
+                }
+                if (b0 + lane < p.n_m_blk) cum[b0 + lane + 1] = base + incl;
+                base += __shfl_sync(0xffffffffu, incl, 31);
+            }
+            if (lane == 0) cum[0] = 0;
+        }
+        __syncthreads();
+    }
+    const int n_tiles = LIST ? cum[LIST ? p.n_m_blk : 0] : p.n_tiles;
+    // (LIST) item t: its 128-row tile and its two blocks (second: -1 when there is none)
+    auto list_item = [&](int t, int* tile, int* blk) {
+        int lo = 0, hi = p.n_m_blk;          // the last row block with cum <= t
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (cum[mid] <= t) lo = mid;
+            else hi = mid;
+        }
+        const int i = t - cum[lo], c = p.cnt[lo];
+        *tile = 2 * lo + (i & 1);
+        const int at = i & ~1;
+        blk[0] = p.list[(size_t)lo * p.n_list + at] & 0xFFFF;
+        blk[1] = at + 1 < c ? p.list[(size_t)lo * p.n_list + at + 1] & 0xFFFF : -1;
+    };
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1317,13 +1399,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             int s = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int t = pair; t < p.n_tiles && ok; t += n_pairs) {
+            for (int t = pair; t < n_tiles && ok; t += n_pairs) {
+                int tile = t, blk[2] = {0, -1};
+                if constexpr (LIST) list_item(t, &tile, blk);
                 for (int i = 0; i < n_kb; ++i) {
                     if (!mbar_wait(empty(s), ph ^ 1u, abort_f, p.err, p.wait_cycles)) { ok = false; break; }
                     const uint32_t sa = base + s * STAGE_BYTES;
-                    mbar_expect_tx(full(s), STAGE_BYTES);
-                    tma_load_2d(sa, &tmA, full(s), (kb0 + i) * BK, t * BM);
-                    tma_load_2d(sa + A_BYTES, &tmB, full(s), (kb0 + i) * BK, 0);
+                    const uint32_t half = LIST && blk[1] < 0 ? TS::B_BYTES / 2 : 0;
+                    mbar_expect_tx(full(s), STAGE_BYTES - half);
+                    tma_load_2d(sa, &tmA, full(s), (kb0 + i) * BK, tile * BM);
+                    tma_load_2d(sa + A_BYTES, &tmB, full(s), (kb0 + i) * BK, LIST ? blk[0] * 64 : 0);
+                    if (LIST && blk[1] >= 0)
+                        tma_load_2d(sa + A_BYTES + TS::B_BYTES / 2, &tmB, full(s), (kb0 + i) * BK,
+                                    blk[1] * 64);
                     ++n_armed;
                     if (++s == STAGES) { s = 0; ph ^= 1u; }
                 }
@@ -1334,7 +1422,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             int s = 0;
             uint32_t ph = 0, tph = 0;
             bool ok = true;
-            for (int t = pair; t < p.n_tiles && ok; t += n_pairs) {
+            for (int t = pair; t < n_tiles && ok; t += n_pairs) {
                 if (!mbar_wait(tempty, tph ^ 1u, abort_f, p.err, p.wait_cycles)) break;
                 tc_fence_after();
                 for (int i = 0; i < n_kb; ++i) {
@@ -1364,10 +1452,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         const uint32_t peer_free = map_rank(part_free, 1);
         uint32_t tph = 0;
         int i = 0;
-        for (int t = pair; t < p.n_tiles; t += n_pairs, ++i) {
+        for (int t = pair; t < n_tiles; t += n_pairs, ++i) {
             if (!mbar_wait(tfull, tph, abort_f, p.err, p.wait_cycles)) break;
             tc_fence_after();
-            const int m = t * BM + r;
+            int tile = t, blk[2] = {0, -1};
+            if constexpr (LIST) list_item(t, &tile, blk);
+            const int m = tile * BM + r;
             bool ok = true;
             if (rank == 1) {
                 // the previous tile's half has been read before this one overwrites it
@@ -1378,6 +1468,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                     for (int c = 0; c < BNT / 32; ++c) {
                         float v[32];
                         tmem_ld32(t_row + (uint32_t)(c * 32), v);
+                        if (LIST && n_kb == 0) {             // K of one block: the even CTA has it
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+                        }
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
                             st_cluster_v4(part_row + (uint32_t)((c * 32 + 4 * q) * 4), v[4 * q],
@@ -1394,9 +1488,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                     const float* pr = part + (size_t)r * TS::PART_LD;
                     float dummy_max = 0.f, dummy_sum = 0.f;
                     int dummy_arg = 0;
+                    int lo = 0, hi = 0;                      // (LIST) columns of the row's adapter
+                    float sc = 0.f;
+                    if (LIST && m < p.M) {
+                        const int id = p.ids[m];
+                        if (id >= 0 && id < p.n_adapters) {
+                            lo = id * p.ad_rank;
+                            hi = lo + p.ad_rank;
+                            sc = p.ad_scale[id];
+                        }
+                    }
                     for (int c = 0; c < BNT / 32; ++c) {
                         const int n = c * 32;
-                        if (n >= p.N) break;                 // warp-uniform
+                        if (LIST ? blk[c >> 1] < 0 : n >= p.N) break;        // warp-uniform
                         float v[32];
                         tmem_ld32(t_row + (uint32_t)n, v);
 #pragma unroll
@@ -1404,7 +1508,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                             const float4 o = *reinterpret_cast<const float4*>(pr + n + 4 * q);
                             v[4 * q] += o.x; v[4 * q + 1] += o.y; v[4 * q + 2] += o.z; v[4 * q + 3] += o.w;
                         }
-                        epilogue_chunk<EPI_SHRINK>(p, m, n, v, &dummy_max, &dummy_sum, &dummy_arg);
+                        if constexpr (LIST) {
+                            const int col = blk[c >> 1] * 64 + (c & 1) * 32;
+                            if (m < p.M) {
+                                uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.C) +
+                                                                      (size_t)m * p.ldc + col);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    v[j] = col + j >= lo && col + j < hi ? v[j] * sc : 0.f;
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    out[q] = make_uint4(pack2_bf16(v[8 * q], v[8 * q + 1]),
+                                                        pack2_bf16(v[8 * q + 2], v[8 * q + 3]),
+                                                        pack2_bf16(v[8 * q + 4], v[8 * q + 5]),
+                                                        pack2_bf16(v[8 * q + 6], v[8 * q + 7]));
+                            }
+                        } else {
+                            epilogue_chunk<EPI_SHRINK>(p, m, n, v, &dummy_max, &dummy_sum, &dummy_arg);
+                        }
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(peer_free);
@@ -1556,23 +1677,23 @@ int launch_shrink_pair(const CUtensorMap& a, const CUtensorMap& b, const TcParam
     constexpr int smem = TileS<BNT>::SMEM_BYTES;
     static bool attr = false;
     if (!attr) {
-        if (cudaFuncSetAttribute(shrink_pair_kernel<BNT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(shrink_pair_kernel<BNT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  smem) != cudaSuccess)
             return 1;
         attr = true;
     }
     int pairs = num_sms() / 2;
     if (p.n_tiles < pairs) pairs = p.n_tiles;
-    shrink_pair_kernel<BNT><<<2 * pairs, NUM_THREADS, smem, st>>>(a, b, p);
+    shrink_pair_kernel<BNT, false><<<2 * pairs, NUM_THREADS, smem, st>>>(a, b, p);
     return cudaGetLastError() == cudaSuccess ? 0 : 1;
 }
 
-template <int EPI, bool F8, bool SPLIT = false>
+template <int EPI, bool F8, bool SPLIT = false, bool LIST = false>
 int launch_epi2(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a2,
                 const CUtensorMap& b2, const CUtensorMap& c, const TcParams& p, cudaStream_t st) {
     static bool attr = false;
     if (!attr) {
-        if (cudaFuncSetAttribute(gemm_tc2_kernel<EPI, F8, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(gemm_tc2_kernel<EPI, F8, SPLIT, LIST>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  SMEM2_BYTES) != cudaSuccess)
             return 1;
         attr = true;
@@ -1590,14 +1711,14 @@ int launch_epi2(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a
         cfg.attrs = at;
         cfg.numAttrs = 1;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, gemm_tc2_kernel<EPI, F8, SPLIT>, &cfg) != cudaSuccess || n <= 0)
+        if (cudaOccupancyMaxActiveClusters(&n, gemm_tc2_kernel<EPI, F8, SPLIT, LIST>, &cfg) != cudaSuccess || n <= 0)
             n = num_sms() / 2;
         max_pairs = n;
     }
     int pairs = max_pairs;
     const int items = SPLIT ? p.n_tiles * p.ksplit : p.n_tiles;
     if (items < pairs) pairs = items;
-    gemm_tc2_kernel<EPI, F8, SPLIT><<<2 * pairs, NUM_THREADS, SMEM2_BYTES, st>>>(a, b, a2, b2, c, p);
+    gemm_tc2_kernel<EPI, F8, SPLIT, LIST><<<2 * pairs, NUM_THREADS, SMEM2_BYTES, st>>>(a, b, a2, b2, c, p);
     return cudaGetLastError() == cudaSuccess ? 0 : 1;
 }
 
@@ -1756,7 +1877,9 @@ int launch_split_reduce(const GemmArgs& g, const TcParams& p, int ks, cudaStream
             e = cudaGetLastError();
         }
     };
-    if (g.epi == EPI_SHRINK) {
+    if (g.adapt) {
+        e = launch_adapter_reduce(*g.adapt, g.adapt_S, g.ws, ks, st, pdl);
+    } else if (g.epi == EPI_SHRINK) {
         launch_shrink_rows_sum(g.ws, ks, g.M, g.N, g.C, g.ldc, g.c_type, g.row_sign, g.eps,
                                g.scale_cols, g.a_scale, st, pdl);
         e = cudaGetLastError();
@@ -1825,6 +1948,7 @@ int gemm_tc_swapped(const GemmArgs& g, cudaStream_t st) {
     if (cudaGetSymbolAddress(reinterpret_cast<void**>(&err), g_tc_error) != cudaSuccess) return 1;
     p.err = err;
     p.wait_cycles = g_wait_cycles;
+    p.dep_late = g.adapt != nullptr;         // the kernel before is the adapters' shrink
     // K splits: the weight stream is the cost.  In units of one 128 x 64 weight block, the
     // busiest SM streams rounds x (kbs + slice) blocks at up to SM_BW_REL times its fair share
     // of HBM, and all SMs together stream the weights plus the slices written and read back;
@@ -1996,8 +2120,8 @@ int gemm_tc(const GemmArgs& g, cudaStream_t st) {
         int ks = (2 * pairs + p.n_tiles - 1) / p.n_tiles;
         ks = std::min(ks, std::min(8, p.kb_main / 4));
         while (ks > 1 && (size_t)ks * g.M * g.N > g.ws_floats) --ks;
-        if (ks > 1) ks = effective_splits(p.kb_main, ks, &p.kbs);   // no split without K blocks
-        if (ks > 1) {
+        if (ks > 1 || g.adapt) ks = effective_splits(p.kb_main, max(ks, 1), &p.kbs);   // no split without K blocks
+        if (ks > 1 || g.adapt) {
             p.ksplit = ks;
             CUtensorMap c;
             if (!make_map_ws(&c, g.ws, ks, g.M, g.N)) return 1;
@@ -2046,6 +2170,48 @@ long long gemm_tc_set_wait_cycles(long long cycles) {
     const long long old = g_wait_cycles;
     g_wait_cycles = cycles > 0 ? cycles : WAIT_CYCLES;
     return old;
+}
+
+int gemm_tc_adapters(const AdapterArgs& a, const AdapterTiles& t, cudaStream_t st) {
+    const int K2 = a.n_adapters * a.rank;
+    const int blocks = (a.M + BM2 - 1) / BM2;
+    if (blocks > MAX_LIST_BLOCKS) return 1;
+    CUtensorMap x, f, w, s2, b2, c;
+    if (!make_map(&x, a.x, a.M, a.K, a.K, BM) || !make_map(&f, a.A, K2, a.K, a.K, 64) ||
+        !make_map(&w, a.W, a.N, a.K, a.K, 128) || !make_map(&s2, t.S, a.M, t.ldS, t.ldS, BM) ||
+        !make_map(&b2, a.B, a.N, K2, K2, 128) || !make_map_out(&c, a.y, a.M, a.N, a.N, a.accumulate != 0))
+        return 1;
+    TcParams p;
+    memset(&p, 0, sizeof(p));
+    p.M = a.M; p.N = K2;
+    p.kb_main = (a.K + BK - 1) / BK;
+    p.n_m_blk = blocks;
+    p.C = t.S; p.ldc = t.ldS; p.c_type = E_BF16;
+    p.cnt = t.cnt; p.list = t.list; p.n_list = t.n_list;
+    p.ids = a.ids; p.ad_scale = a.scale; p.n_adapters = a.n_adapters; p.ad_rank = a.rank;
+    int* err = nullptr;
+    if (cudaGetSymbolAddress(reinterpret_cast<void**>(&err), g_tc_error) != cudaSuccess) return 1;
+    p.err = err;
+    p.wait_cycles = g_wait_cycles;
+    constexpr int smem = TileS<128>::SMEM_BYTES;
+    if (cudaFuncSetAttribute(shrink_pair_kernel<128, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem) != cudaSuccess)
+        return 1;
+    const int items = 2 * blocks * ((t.n_list + 1) / 2);     // at most
+    const int pairs = std::min(items, num_sms() / 2);
+    if (launch_pdl(shrink_pair_kernel<128, true>, dim3(2 * pairs), dim3(NUM_THREADS), smem, st, x, f, p) !=
+        cudaSuccess)
+        return 1;
+    p.N = a.N;
+    p.group_m = 12;
+    p.n_n_blk = (a.N + BN - 1) / BN;
+    p.n_tiles = blocks * p.n_n_blk;
+    p.bias = a.bias;
+    p.C = a.y; p.ldc = a.N; p.c_type = a.accumulate ? E_F32 : E_BF16;
+    p.odd = t.odd;
+    if (a.accumulate) return launch_epi2<EPI_RESID, false, false, true>(x, w, s2, b2, c, p, st);
+    return a.act ? launch_epi2<EPI_STORE_RELU, false, false, true>(x, w, s2, b2, c, p, st)
+                 : launch_epi2<EPI_STORE, false, false, true>(x, w, s2, b2, c, p, st);
 }
 
 int gemm_tc_error_word() {

@@ -104,6 +104,16 @@ struct KvAppend {
     int q_dim, kv2;
 };
 
+// One adapter per row (zo_ops.h, zo_op_linear_adapters).
+struct AdapterArgs {
+    const void* x; const void* W; const float* bias; const void* A; const void* B;
+    const int* ids; const float* scale;
+    int n_adapters, rank;
+    void* y; int M, N, K;
+    int dtype, act, accumulate;
+    void* ws; size_t ws_bytes;
+};
+
 struct GemmArgs {
     const void* A; int lda; int a_type;     // [M x K], K contiguous
     const void* B; int ldb; int b_type;     // [N x K], K contiguous
@@ -140,6 +150,9 @@ struct GemmArgs {
     // EPI_STORE / EPI_QKNR with a split reduction: the reduction may also append the k|v
     // columns to the cache (sets *kv_done = 1; else the caller copies them)
     const KvAppend* kv_append; int* kv_done;
+    // a split reduction that also adds each row's own adapter (see AdapterArgs; then launched
+    // behind the kernel that writes adapt_S): bias, activation and output are the adapters'
+    const AdapterArgs* adapt; const float* adapt_S;
 };
 // Split-K residual reduction with the next norm fused (see NormNext); false when the shape or
 // alignment is outside the vectorised form (nothing launched).
@@ -211,16 +224,18 @@ size_t paged_chunk_workspace(int hd);
 int paged_chunk_error_word();
 
 // ---- serving: one adapter per row ----------------------------------------------------------
-struct AdapterArgs {
-    const void* x; const void* W; const float* bias; const void* A; const void* B;
-    const int* ids; const float* scale;
-    int n_adapters, rank;
-    void* y; int M, N, K;
-    int dtype, act, accumulate;
-    void* ws; size_t ws_bytes;
-};
 size_t adapter_workspace(int M, int N, int K, int n_adapters, int rank, int dtype);
 cudaError_t launch_linear_adapters_simt(const AdapterArgs& a, cudaStream_t st);
+bool linear_adapters_tc_supported(const AdapterArgs& a);
+cudaError_t launch_linear_adapters_tc(const AdapterArgs& a, cudaStream_t st);
+// y rows from ks fp32 slices ws[ks][M][N], their own adapter's S[m] B_a^T (S fp32 [M x rank]),
+// bias and activation; pdl: a programmatic dependent of the kernel that wrote the slices
+cudaError_t launch_adapter_reduce(const AdapterArgs& a, const float* S, const float* ws, int ks,
+                                  cudaStream_t st, bool pdl);
+// Row blocks of 256: the 64-column blocks of the factors that their rows' adapters touch (cnt,
+// list: see TcParams), the masked shrink S [M x ldS] bf16 and the marks of chunks to repair.
+struct AdapterTiles { const int* cnt; const int* list; int n_list; void* S; int ldS; uint8_t* odd; };
+int gemm_tc_adapters(const AdapterArgs& a, const AdapterTiles& t, cudaStream_t st);   // 0 ok
 
 // ---- objective, estimator, update ------------------------------------------------------
 void launch_lse_merge(const float* part_max, const float* part_sum, const float* tgt_logit,

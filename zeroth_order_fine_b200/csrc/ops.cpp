@@ -414,6 +414,11 @@ int zo_op_linear_adapters(const void* x, const void* W, const float* bias, const
     a.dtype = dtype == ZO_DTYPE_BF16 ? E_BF16 : E_F32;
     a.act = act; a.accumulate = accumulate;
     a.ws = ws; a.ws_bytes = ws_bytes;
+    if (impl != ZO_IMPL_CUDA_CORES && linear_adapters_tc_supported(a)) {
+        if (launch_linear_adapters_tc(a, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+            return op_fail("adapter linear launch failed");
+        return ZO_OK;
+    }
     if (impl == ZO_IMPL_TENSOR_CORES) return ZO_ERR_UNSUPPORTED;
     if (launch_linear_adapters_simt(a, static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return op_fail("adapter linear launch failed");
