@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "kernels.h"
 
 namespace zo {
@@ -60,6 +62,19 @@ __device__ __forceinline__ float block_max(float v, float* red /* >= 32 floats *
 }
 
 inline unsigned cdiv(long long a, long long b) { return (unsigned)((a + b - 1) / b); }
+
+// Raises a kernel's dynamic shared memory limit, once per device (the attribute belongs to the
+// device's copy of the kernel): done holds one bit per device.
+inline cudaError_t smem_limit(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // ---- debug build (ZO_DEBUG): device bounds checks -------------------------------------
 // ZO_DCHECK(cond, bit) is `cond` in the debug build, where a failed check also ORs `bit` into

@@ -122,11 +122,31 @@ __device__ __forceinline__ void bf8(const uint4& u, float* f) {
 }
 
 // The fp32 shrink of the rows' own adapters (direct form): one warp per (m, j), 16-byte loads;
-// the warps of a CTA share row m through L1.
+// the warps of a CTA share row m through L1.  The CTAs behind those (FETCH_CTAS of them) ask L2 for
+// the rows' expand factors, output row by output row, while the product streams W: the reduction
+// reads them in 2 rank-byte pieces, which from HBM, each by itself, took it 15 us instead of 6 (48
+// rows, 32 adapters of rank 16, OPT-13B q|k|v).
+constexpr int FETCH_CTAS = 148;
 __global__ void __launch_bounds__(SH_WARPS * 32) adapter_shrink_rows_kernel(AdapterArgs a, float* S) {
     grid_dep_launch();                 // the product does not read S: it may start now
-    const int m = blockIdx.x, lane = threadIdx.x & 31;
-    const int j = blockIdx.y * SH_WARPS + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, groups = (a.rank + SH_WARPS - 1) / SH_WARPS;
+    const int fetch = (int)blockIdx.x - a.M * groups;
+    if (fetch >= 0) {
+        const size_t ldb = (size_t)a.n_adapters * a.rank * 2;
+        for (int m0 = 0; m0 < a.M; m0 += 32) {
+            const int id = m0 + lane < a.M ? a.ids[m0 + lane] : -1;
+            // one lane per adapter of these rows
+            const unsigned same = __match_any_sync(0xffffffffu, id);
+            if (id < 0 || id >= a.n_adapters || (same & ((1u << lane) - 1u))) continue;
+            const char* b = static_cast<const char*>(a.B) + (size_t)id * a.rank * 2;
+            for (int n = fetch * SH_WARPS + (threadIdx.x >> 5); n < a.N; n += FETCH_CTAS * SH_WARPS)
+                for (int c = 0; c < a.rank * 2; c += 32)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(b + (size_t)n * ldb + c));
+        }
+        return;
+    }
+    const int m = (int)blockIdx.x / groups;
+    const int j = (int)blockIdx.x % groups * SH_WARPS + (threadIdx.x >> 5);
     const int id = a.ids[m];
     if (id < 0 || id >= a.n_adapters || j >= a.rank) return;
     const uint4* x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + (size_t)m * a.K);
@@ -167,54 +187,76 @@ __device__ __forceinline__ void adapter_store4(const AdapterArgs& a, int m, int 
     }
 }
 
-// y += S[m] B_a[n .. n + 3]^T for the row's own adapter; NaN for an id that is none
-__device__ __forceinline__ void adapter_expand4(const AdapterArgs& a, const float* __restrict__ S, int m,
-                                                int n, float* y) {
-    const int id = a.ids[m];
-    if (id == -1) return;
-    if (id < 0 || id >= a.n_adapters) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = __int_as_float(0x7fc00000);
-        return;
-    }
-    const size_t ldb = (size_t)a.n_adapters * a.rank;
-    const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(a.B) + (size_t)n * ldb + (size_t)id * a.rank;
-    const float* s = S + (size_t)m * a.rank;
-    if (a.rank % 8 == 0) {
-#pragma unroll 2
-        for (int c = 0; c < a.rank; c += 8) {
-            const float4 s0 = *reinterpret_cast<const float4*>(s + c), s1 = *reinterpret_cast<const float4*>(s + c + 4);
-            const float sv[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
+// The slices' reduction of the direct form: a CTA takes 512 columns of a row.  First the expand
+// S[m] B_a[n]^T of its columns into shared memory: LPR lanes share a row of B (LPR 16-byte loads side
+// by side, so that a warp's load takes whole sectors), their sums joined by shuffles.  Then
+// each thread adds the slices of 4 columns in split order, the expand, bias and activation.
+template <int LPR>
+__device__ __forceinline__ void adapter_expand(const AdapterArgs& a, const float* __restrict__ s,
+                                               const __nv_bfloat16* __restrict__ b, size_t ldb, int n0,
+                                               int n1, float* e) {
+    constexpr int ROWS = 32 / LPR;            // rows of B per warp and load
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = lane % LPR;
+#pragma unroll 4
+    for (int i = 0; i < 128; i += ROWS) {
+        const int n = n0 + warp * 128 + i + lane / LPR;
+        float y = 0.f;
+        if (n < n1)
+            for (int c = part * 8; c < a.rank; c += LPR * 8) {
                 float bv[8];
-                bf8(__ldg(reinterpret_cast<const uint4*>(b + i * ldb + c)), bv);
+                bf8(__ldg(reinterpret_cast<const uint4*>(b + n * ldb + c)), bv);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) y[i] = fmaf(sv[q], bv[q], y[i]);
+                for (int q = 0; q < 8; ++q) y = fmaf(s[c + q], bv[q], y);
             }
-        }
-    } else {
-        for (int c = 0; c < a.rank; ++c)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = fmaf(s[c], __bfloat162float(b[i * ldb + c]), y[i]);
+        for (int d = LPR / 2; d > 0; d >>= 1) y += __shfl_xor_sync(0xffffffffu, y, d);
+        if (part == 0) e[warp * 128 + i + lane / LPR] = y;
     }
 }
 
-// The slices' reduction of the direct form: one thread per 4 columns of a row; the slices are
-// added in split order.
 __global__ void __launch_bounds__(128)
     adapter_reduce_kernel(AdapterArgs a, const float* __restrict__ S, const float* __restrict__ ws, int ks) {
+    __shared__ __align__(16) float e[512];
+    __shared__ float s[256];
+    const int m = blockIdx.y, n0 = blockIdx.x * 512, n = n0 + threadIdx.x * 4;
+    const int id = a.ids[m];
+    const bool live = id >= 0 && id < a.n_adapters;
     grid_dep_wait();
-    const int m = blockIdx.y;
-    const int n = (blockIdx.x * blockDim.x + threadIdx.x) * 4;
-    if (n >= a.N) return;
     float y[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < ks; ++s) {
-        const float4 w = *reinterpret_cast<const float4*>(ws + ((size_t)s * a.M + m) * a.N + n);
-        y[0] += w.x; y[1] += w.y; y[2] += w.z; y[3] += w.w;
+    if (n < a.N)
+        for (int k = 0; k < ks; ++k) {
+            const float4 w = *reinterpret_cast<const float4*>(ws + ((size_t)k * a.M + m) * a.N + n);
+            y[0] += w.x; y[1] += w.y; y[2] += w.z; y[3] += w.w;
+        }
+    if (live) {
+        for (int c = threadIdx.x; c < a.rank; c += 128) s[c] = S[(size_t)m * a.rank + c];
+        __syncthreads();
+        const size_t ldb = (size_t)a.n_adapters * a.rank;
+        const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(a.B) + (size_t)id * a.rank;
+        const int n1 = min(a.N, n0 + 512);
+        if (a.rank % 64 == 0) {
+            adapter_expand<8>(a, s, b, ldb, n0, n1, e);
+        } else if (a.rank % 16 == 0) {
+            adapter_expand<2>(a, s, b, ldb, n0, n1, e);
+        } else if (a.rank % 8 == 0) {
+            adapter_expand<1>(a, s, b, ldb, n0, n1, e);
+        } else {
+            for (int i = threadIdx.x; n0 + i < n1; i += 128) {
+                float v = 0.f;
+                for (int c = 0; c < a.rank; ++c) v = fmaf(s[c], __bfloat162float(b[(n0 + i) * ldb + c]), v);
+                e[i] = v;
+            }
+        }
+        __syncthreads();
+        if (n < a.N) {
+            const float4 v = *reinterpret_cast<const float4*>(e + threadIdx.x * 4);
+            y[0] += v.x; y[1] += v.y; y[2] += v.z; y[3] += v.w;
+        }
+    } else if (id != -1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = __int_as_float(0x7fc00000);
     }
-    adapter_expand4(a, S, m, n, y);
-    adapter_store4(a, m, n, y);
+    if (n < a.N) adapter_store4(a, m, n, y);
 }
 
 // The tiles form's lists: CTA = a block of 256 rows, thread = a row.  A block's list holds the
@@ -269,6 +311,10 @@ __global__ void __launch_bounds__(FIX_THREADS)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int id_l = m0 + lane < a.M ? a.ids[m0 + lane] : -1;
     const unsigned none = __ballot_sync(0xffffffffu, id_l < -1 || id_l >= a.n_adapters);
+    // usually nothing is marked: all of the CTA's marks in one look
+    int any = none != 0u;
+    for (int c = threadIdx.x; c < chunks; c += FIX_THREADS) any |= odd[(size_t)blockIdx.x * chunks + c];
+    if (!__syncthreads_or(any)) return;
     for (int c = warp; c < chunks; c += FIX_THREADS / 32) {
         const bool marked = odd[(size_t)blockIdx.x * chunks + c] != 0;
         if (!marked && !none) continue;
@@ -372,7 +418,7 @@ cudaError_t launch_linear_adapters_simt(const AdapterArgs& a, cudaStream_t st) {
 
 cudaError_t launch_adapter_reduce(const AdapterArgs& a, const float* S, const float* ws, int ks,
                                   cudaStream_t st, bool pdl) {
-    const dim3 grid(cdiv(a.N / 4, 128), a.M);
+    const dim3 grid(cdiv(a.N, 512), a.M);
     if (pdl) return launch_pdl(adapter_reduce_kernel, grid, dim3(128), 0, st, a, S, ws, ks);
     adapter_reduce_kernel<<<grid, 128, 0, st>>>(a, S, ws, ks);
     return cudaGetLastError();
@@ -403,7 +449,7 @@ cudaError_t launch_linear_adapters_tc(const AdapterArgs& a, cudaStream_t st) {
         g.adapt = &a;
         g.adapt_S = S;
         if (!gemm_tc_supported(g)) return cudaErrorNotSupported;
-        adapter_shrink_rows_kernel<<<dim3(a.M, cdiv(a.rank, SH_WARPS)), SH_WARPS * 32, 0, st>>>(a, S);
+        adapter_shrink_rows_kernel<<<a.M * cdiv(a.rank, SH_WARPS) + FETCH_CTAS, SH_WARPS * 32, 0, st>>>(a, S);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         return gemm_tc(g, st) ? cudaErrorUnknown : cudaSuccess;

@@ -1619,6 +1619,19 @@ bool make_map_out(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// g_tc_error on the current device (looked up once per device)
+int* error_word_address() {
+    static std::atomic<int*> at[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+    int* p = dev < 64 ? at[dev].load(std::memory_order_acquire) : nullptr;
+    if (!p) {
+        if (cudaGetSymbolAddress(reinterpret_cast<void**>(&p), g_tc_error) != cudaSuccess) return nullptr;
+        if (dev < 64) at[dev].store(p, std::memory_order_release);
+    }
+    return p;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int num_sms() {
@@ -1636,13 +1649,8 @@ template <int EPI, int BNT, bool F8 = false>
 int launch_epi(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a2,
                const CUtensorMap& b2, const TcParams& p, cudaStream_t st) {
     constexpr int smem = Tile1<BNT>::SMEM_BYTES;
-    static bool attr = false;
-    if (!attr) {
-        if (cudaFuncSetAttribute(gemm_tc_kernel<EPI, BNT, F8>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-            return 1;
-        attr = true;
-    }
+    static std::atomic<uint64_t> attr{0};
+    if (smem_limit(reinterpret_cast<const void*>(gemm_tc_kernel<EPI, BNT, F8>), smem, attr) != cudaSuccess) return 1;
     const int items = EPI == EPI_SPLIT_T ? p.n_tiles * p.ksplit : p.n_tiles;
     const int grid = items < num_sms() ? items : num_sms();
     if (EPI == EPI_SPLIT_T)
@@ -1675,13 +1683,8 @@ template <int BNT>
 int launch_shrink_pair(const CUtensorMap& a, const CUtensorMap& b, const TcParams& p,
                        cudaStream_t st) {
     constexpr int smem = TileS<BNT>::SMEM_BYTES;
-    static bool attr = false;
-    if (!attr) {
-        if (cudaFuncSetAttribute(shrink_pair_kernel<BNT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 smem) != cudaSuccess)
-            return 1;
-        attr = true;
-    }
+    static std::atomic<uint64_t> attr{0};
+    if (smem_limit(reinterpret_cast<const void*>(shrink_pair_kernel<BNT, false>), smem, attr) != cudaSuccess) return 1;
     int pairs = num_sms() / 2;
     if (p.n_tiles < pairs) pairs = p.n_tiles;
     shrink_pair_kernel<BNT, false><<<2 * pairs, NUM_THREADS, smem, st>>>(a, b, p);
@@ -1691,13 +1694,8 @@ int launch_shrink_pair(const CUtensorMap& a, const CUtensorMap& b, const TcParam
 template <int EPI, bool F8, bool SPLIT = false, bool LIST = false>
 int launch_epi2(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a2,
                 const CUtensorMap& b2, const CUtensorMap& c, const TcParams& p, cudaStream_t st) {
-    static bool attr = false;
-    if (!attr) {
-        if (cudaFuncSetAttribute(gemm_tc2_kernel<EPI, F8, SPLIT, LIST>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 SMEM2_BYTES) != cudaSuccess)
-            return 1;
-        attr = true;
-    }
+    static std::atomic<uint64_t> attr{0};
+    if (smem_limit(reinterpret_cast<const void*>(gemm_tc2_kernel<EPI, F8, SPLIT, LIST>), SMEM2_BYTES, attr) != cudaSuccess) return 1;
     static int max_pairs = 0;
     if (!max_pairs) {
         // SM pairs that can be resident at once (clusters of 2 stay inside a GPC)
@@ -1944,8 +1942,8 @@ int gemm_tc_swapped(const GemmArgs& g, cudaStream_t st) {
     p.tok_pos = g.tok_pos; p.qn = g.qn; p.kn = g.kn;
     p.rope_cos = g.rope_cos; p.rope_sin = g.rope_sin; p.norm_eps = g.norm_eps;
     p.n_q_heads = g.n_q_heads; p.n_qk_heads = g.n_qk_heads;
-    int* err = nullptr;
-    if (cudaGetSymbolAddress(reinterpret_cast<void**>(&err), g_tc_error) != cudaSuccess) return 1;
+    int* err = error_word_address();
+    if (!err) return 1;
     p.err = err;
     p.wait_cycles = g_wait_cycles;
     p.dep_late = g.adapt != nullptr;         // the kernel before is the adapters' shrink
@@ -2095,8 +2093,8 @@ int gemm_tc(const GemmArgs& g, cudaStream_t st) {
     p.tok_pos = g.tok_pos; p.qn = g.qn; p.kn = g.kn;
     p.rope_cos = g.rope_cos; p.rope_sin = g.rope_sin; p.norm_eps = g.norm_eps;
     p.n_q_heads = g.n_q_heads; p.n_qk_heads = g.n_qk_heads;
-    int* err = nullptr;
-    if (cudaGetSymbolAddress(reinterpret_cast<void**>(&err), g_tc_error) != cudaSuccess) return 1;
+    int* err = error_word_address();
+    if (!err) return 1;
     p.err = err;
     p.wait_cycles = g_wait_cycles;
     if (g.epi == EPI_SHRINK && !g.ws && !f8 && g.K2 == 0 && bnt <= 128 && p.kb_main >= 2) {
@@ -2189,13 +2187,13 @@ int gemm_tc_adapters(const AdapterArgs& a, const AdapterTiles& t, cudaStream_t s
     p.C = t.S; p.ldc = t.ldS; p.c_type = E_BF16;
     p.cnt = t.cnt; p.list = t.list; p.n_list = t.n_list;
     p.ids = a.ids; p.ad_scale = a.scale; p.n_adapters = a.n_adapters; p.ad_rank = a.rank;
-    int* err = nullptr;
-    if (cudaGetSymbolAddress(reinterpret_cast<void**>(&err), g_tc_error) != cudaSuccess) return 1;
+    int* err = error_word_address();
+    if (!err) return 1;
     p.err = err;
     p.wait_cycles = g_wait_cycles;
     constexpr int smem = TileS<128>::SMEM_BYTES;
-    if (cudaFuncSetAttribute(shrink_pair_kernel<128, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             smem) != cudaSuccess)
+    static std::atomic<uint64_t> attr{0};
+    if (smem_limit(reinterpret_cast<const void*>(shrink_pair_kernel<128, true>), smem, attr) != cudaSuccess)
         return 1;
     const int items = 2 * blocks * ((t.n_list + 1) / 2);     // at most
     const int pairs = std::min(items, num_sms() / 2);

@@ -328,9 +328,8 @@ __global__ void __launch_bounds__(A_THREADS) paged_attention_kernel(PagedArgs a)
 template <int HD>
 cudaError_t launch_paged_hd(const PagedArgs& a, cudaStream_t st) {
     const size_t smem = sizeof(float) * ((AQ + 2 * AK) * (HD + 4) + AQ * (AK + 4));
-    // per device and cheap beside the launch: no flag that another device would share
-    cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<HD>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> attr{0};
+    cudaError_t e = smem_limit(reinterpret_cast<const void*>(paged_attention_kernel<HD>), (int)smem, attr);
     if (e != cudaSuccess) return e;
     const long long tiles = ((long long)a.n_tokens * a.g + AQ - 1) / AQ + a.n_rows;
     paged_attention_kernel<HD><<<dim3((unsigned)tiles, a.Hkv), A_THREADS, smem, st>>>(a);

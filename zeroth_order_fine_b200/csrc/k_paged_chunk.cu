@@ -98,6 +98,13 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
         }
     }
 }
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok));
+    return ok != 0;
+}
 __device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity) {
     for (uint32_t i = 0; i < DRAIN_POLLS && !bar_try(bar, parity); ++i) __nanosleep(128);
 }
@@ -132,8 +139,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
           "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_wait_ld() {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+// Waits for the thread's TMEM loads; v: the registers of one of them, which nothing may read before
+__device__ __forceinline__ void tmem_wait_ld(uint32_t* v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]),
+                 "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]),
+                 "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]),
+                 "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]),
+                 "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+                 :
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -148,38 +163,72 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
         "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
         : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// two fp32 operations in one instruction, each rounded as by itself
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// One MMA per 16 of the summed dimension.  The descriptors are a base plus constants, so that the
+// issuing thread spends no more on an MMA than the tensor cores do (rebuilt from addresses each time
+// they cost it ~117 cycles a piece, against 64 on the tensor cores).
 template <int HD>
-__device__ __forceinline__ void mma_qk(uint32_t d, uint32_t q, uint32_t k) {
+__device__ __forceinline__ void mma_qk(uint32_t d, uint64_t q, uint64_t k) {
 #pragma unroll
     for (int kk = 0; kk < HD / 16; ++kk) {
-        const uint32_t off = (kk >> 2) * ATOM + (kk & 3) * 32;
+        const uint64_t off = (uint64_t)(((kk >> 2) * ATOM + (kk & 3) * 32) >> 4);
         asm volatile(
             "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
             "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(desc_k(q + off)), "l"(desc_k(k + off)), "r"(IDESC_QK), "r"(kk > 0 ? 1u : 0u)
+            "l"(q + off), "l"(k + off), "r"(IDESC_QK), "r"(kk > 0 ? 1u : 0u)
             : "memory");
     }
 }
 // steps of 16 keys: P from TMEM (bf16 pairs, 8 columns a step), V from shared memory
 template <int HD>
-__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t p, uint32_t v, int steps, bool accum) {
-    for (int kk = 0; kk < steps; ++kk)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-            "r"(p + kk * 8), "l"(desc_mn(v + kk * 2048)), "r"(Geo<HD>::IDESC_PV),
-            "r"((kk > 0 || accum) ? 1u : 0u)
-            : "memory");
+__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t p, uint64_t v, int steps, bool accum) {
+#pragma unroll
+    for (int kk = 0; kk < UK / 16; ++kk)
+        if (kk < steps)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                "r"(p + kk * 8), "l"(v + (uint64_t)(kk * 2048 >> 4)), "r"(Geo<HD>::IDESC_PV),
+                "r"(kk > 0 ? 1u : (uint32_t)accum)
+                : "memory");
 }
 
 // A stretch's part of one item: units [c0, c1) of it; n[t]: units that tile t's rows see any key
@@ -326,7 +375,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer ----------------
-        if (lane == 0) {
+        // the whole warp runs the loop, so that its counters stay uniform; one lane issues
+        const bool leader = elect_one();
+        {
+            const uint64_t dq = desc_k(base), dk = desc_k(ring), dv = desc_mn(ring);
             // Steps run over the stretch's units; at step i tile t's P V of unit i - 1 comes before
             // its Q K of unit i.  Q K of a tile waits for the tile's P V before it (P and S share
             // columns), P V for the softmax.
@@ -334,7 +386,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             bool have_prev = false, ok = true;
             int prev_c = 0, unit = 0;                 // unit: ring position of the current one
             int qi[2] = {0, 0};                       // pieces begun: q_full and o_free phases
-            int si[2] = {0, 0}, pi[2] = {0, 0};       // Q K and P V issued
+            int pi[2] = {0, 0};                       // P V issued
             long long u = u0;
             bool more = true;
             cur = piece_of(a, k, u1 - u);
@@ -351,9 +403,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (head && qi[t] > 1 && !wait_bar(o_free(t), qi[t] & 1, abort_f)) { ok = false; break; }
                         fence_after();
                         const int valid = prev.valid(prev_c);
-                        mma_pv<HD>(t_o(t), t_s(t), ring + (uint32_t)(vs * TILE), (valid + 15) / 16, !head);
+                        if (leader) {
+                            mma_pv<HD>(t_o(t), t_s(t), dv + (uint64_t)(vs * TILE >> 4), (valid + 15) / 16, !head);
+                            commit(pv_done(t));
+                        }
                         issued = true;
-                        commit(pv_done(t));
                         ++pi[t];
                     }
                     if (more && cur.active(t, c)) {
@@ -363,16 +417,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                         if (pi[t] > 0 && !wait_bar(pv_done(t), (pi[t] - 1) & 1, abort_f)) { ok = false; break; }
                         fence_after();
-                        mma_qk<HD>(t_s(t), base + (uint32_t)(t * TILE), ring + (uint32_t)(ks * TILE));
+                        if (leader) {
+                            mma_qk<HD>(t_s(t), dq + (uint64_t)(t * TILE >> 4), dk + (uint64_t)(ks * TILE >> 4));
+                            commit(s_full(t));
+                        }
                         issued = true;
-                        commit(s_full(t));
-                        ++si[t];
                     }
                 }
                 if (!ok) break;
-                if (have_prev) commit(empty(vs));
+                if (have_prev && leader) commit(empty(vs));
                 if (!more) break;
-                commit(empty(ks));
+                if (leader) commit(empty(ks));
                 have_prev = true;
                 prev = cur;
                 prev_c = c;
@@ -388,7 +443,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             if (issued) {
-                commit(drain);                        // every MMA retires before TMEM is freed
+                if (leader) commit(drain);            // every MMA retires before TMEM is freed
                 drain_bar(drain, 0);
             }
         }
@@ -407,7 +462,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const uint4* q = reinterpret_cast<const uint4*>(
                 static_cast<const __nv_bfloat16*>(a.q) + (size_t)(at.q.start + rr / a.g) * a.ld_q +
                 (size_t)(at.head * a.g + rr % a.g) * HD);
-#pragma unroll
+#pragma unroll 8
             for (int ch = 0; ch < HD / 8; ++ch)
                 *reinterpret_cast<uint4*>(qs + (ch >> 3) * ATOM + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) =
                     live ? __ldg(q + ch) : make_uint4(0u, 0u, 0u, 0u);
@@ -422,7 +477,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (p.any(t)) load_q(k);
         while (ok) {
             const Line::Cursor it = k;
-            float m = -FLT_MAX, l[4] = {0.f, 0.f, 0.f, 0.f};
+            float m = -FLT_MAX;
+            uint64_t l[4] = {0ull, 0ull, 0ull, 0ull};  // eight running sums
             bool bad = it.q.bad;
             const int r = it.tile * RB + t * 128 + row;
             const bool live = r < it.q.rows;
@@ -434,19 +490,27 @@ __global__ void __launch_bounds__(THREADS, 1)
                 ++ns;
                 fence_after();
                 bad |= bad_unit[(unit + c - p.c0) & 7] != 0;
-                uint32_t sv[128];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) tmem_ld32(ts + j * 32, sv + j * 32);
-                tmem_wait_ld();
+                // The row is read twice, 32 scores at a time with the next 32 on their way: once for
+                // the maximum, once for the exponentials.  Held at once it does not fit beside
+                // the rest (128 scores spilled).
                 const int cut = lim - c * UK;
-                if (!__all_sync(0xffffffffu, cut >= UK)) {
-#pragma unroll
-                    for (int j = 0; j < 128; ++j)
-                        if (j >= cut) sv[j] = __float_as_uint(-INFINITY);
-                }
+                const bool masked = !__all_sync(0xffffffffu, cut >= UK);
+                uint32_t sv[2][32];
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                tmem_ld32(ts, sv[0]);
 #pragma unroll
-                for (int j = 0; j < 128; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(sv[j]));
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t* v = sv[h & 1];
+                    tmem_wait_ld(v);
+                    tmem_ld32(ts + ((h + 1) & 3) * 32, sv[(h + 1) & 1]);
+                    if (masked) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (h * 32 + j >= cut) v[j] = __float_as_uint(-INFINITY);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(v[j]));
+                }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
                 // the reference moves when the maximum is over 2^8 above it (at first, at once)
                 const bool move = top > m + 8.f;
@@ -459,28 +523,38 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int j = 0; j < HD / 32; ++j) {
                             uint32_t v[32];
                             tmem_ld32(to + j * 32, v);
-                            tmem_wait_ld();
+                            tmem_wait_ld(v);          // (and for the scores on their way)
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
                             tmem_st32(to + j * 32, v);
                         }
                     }
+                    const uint64_t f2 = pair(f, f);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) l[i] *= f;
+                    for (int i = 0; i < 4; ++i) l[i] = fma2(l[i], f2, 0ull);
                     m = mn;
                 }
+                const uint64_t c2 = pair(sl2, sl2), m2 = pair(-m, -m);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t pk[32];
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t* v = sv[h & 1];
+                    tmem_wait_ld(v);
+                    if (h < 3) tmem_ld32(ts + (h + 1) * 32, sv[(h + 1) & 1]);
+                    if (masked) {
 #pragma unroll
-                    for (int j = 0; j < 64; j += 2) {
-                        const float p0 = ex2(fmaf(__uint_as_float(sv[h * 64 + j]), sl2, -m));
-                        const float p1 = ex2(fmaf(__uint_as_float(sv[h * 64 + j + 1]), sl2, -m));
-                        l[j & 3] += p0;
-                        l[(j + 1) & 3] += p1;
+                        for (int j = 0; j < 32; ++j)
+                            if (h * 32 + j >= cut) v[j] = __float_as_uint(-INFINITY);
+                    }
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float2 x = unpair(fma2(pair(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), c2, m2));
+                        const float p0 = ex2(x.x), p1 = ex2(x.y);
+                        l[(j >> 1) & 3] = add2(l[(j >> 1) & 3], pair(p0, p1));
                         pk[j / 2] = pack2(p0, p1);
                     }
-                    tmem_st32(ts + h * 32, pk);
+                    // over scores that have been read: columns 16 h .. of 32 h ..
+                    tmem_st16(ts + h * 16, pk);
                 }
                 tmem_wait_st();
                 const int valid = p.valid(c);
@@ -512,7 +586,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (p.any(t)) load_q(k);
             }
             const bool whole = done.c0 == 0 && done.c1 == it.units;
-            const float lt = bad ? __int_as_float(0x7fc00000) : (l[0] + l[1]) + (l[2] + l[3]);
+            const float2 l2 = unpair(add2(add2(l[0], l[1]), add2(l[2], l[3])));
+            const float lt = bad ? __int_as_float(0x7fc00000) : l2.x + l2.y;
             Part<HD>* slot = part + 2 * w + (done.c0 == 0 ? 1 : 0);
             if (!whole) {
                 slot->m[t * 128 + row] = m;
@@ -539,7 +614,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int j = 0; j < HD / 32; ++j) {
                     uint32_t v[32];
                     tmem_ld32(to + j * 32, v);
-                    tmem_wait_ld();
+                    tmem_wait_ld(v);
                     if (live && whole) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -586,26 +661,47 @@ __global__ void __launch_bounds__(JOIN_THREADS)
     const PagedDesc d = desc[w];
     const int row = blockIdx.y * JOIN_ROWS + (threadIdx.x & 31), dg = threadIdx.x >> 5;
     if (d.pieces <= 0 || row >= d.rows) return;
-    auto piece = [&](int i) -> const Part<HD>& { return part[2 * (w + i) + (i == 0 ? 1 : 0)]; };
-    float m = -FLT_MAX, l = 0.f;
-    for (int i = 0; i < d.pieces; ++i) m = fmaxf(m, piece(i).m[row]);
     constexpr int DG = HD / 4 / (JOIN_THREADS / 32);  // float4 groups of a thread
+    constexpr int N = 4;                              // pieces in flight together
+    float m = -FLT_MAX, l = 0.f;
     float4 o[DG];
 #pragma unroll
     for (int j = 0; j < DG; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < d.pieces; ++i) {
-        const Part<HD>& p = piece(i);
-        const float li = p.l[row];
-        if (li == 0.f) continue;
-        const float f = ex2(p.m[row] - m);
-        l = fmaf(f, li, l);
+    for (int i0 = 0; i0 < d.pieces; i0 += N) {
+        float pm[N], pl[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const Part<HD>* p = part + 2 * (w + i0 + i) + (i0 + i == 0 ? 1 : 0);
+            pm[i] = i0 + i < d.pieces ? p->m[row] : -FLT_MAX;
+            pl[i] = i0 + i < d.pieces ? p->l[row] : 0.f;
+        }
+        float mn = m;
+#pragma unroll
+        for (int i = 0; i < N; ++i) mn = fmaxf(mn, pm[i]);
+        const float g = ex2(m - mn);
+        m = mn;
+        l *= g;
 #pragma unroll
         for (int j = 0; j < DG; ++j) {
-            const float4 v = p.o[dg * DG + j][row];
-            o[j].x = fmaf(f, v.x, o[j].x);
-            o[j].y = fmaf(f, v.y, o[j].y);
-            o[j].z = fmaf(f, v.z, o[j].z);
-            o[j].w = fmaf(f, v.w, o[j].w);
+            o[j].x *= g;
+            o[j].y *= g;
+            o[j].z *= g;
+            o[j].w *= g;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (pl[i] == 0.f) continue;
+            const Part<HD>* p = part + 2 * (w + i0 + i) + (i0 + i == 0 ? 1 : 0);
+            const float f = ex2(pm[i] - m);
+            l = fmaf(f, pl[i], l);
+#pragma unroll
+            for (int j = 0; j < DG; ++j) {
+                const float4 v = p->o[dg * DG + j][row];
+                o[j].x = fmaf(f, v.x, o[j].x);
+                o[j].y = fmaf(f, v.y, o[j].y);
+                o[j].z = fmaf(f, v.z, o[j].z);
+                o[j].w = fmaf(f, v.w, o[j].w);
+            }
         }
     }
     const float inv = 1.f / l;
@@ -623,12 +719,12 @@ cudaError_t launch_chunk(const PagedArgs& a, cudaStream_t st) {
     CUtensorMap map;
     const int box_rows = min(UK, 1 << a.page_shift);
     if (!paged_cache_map(&map, a, box_rows, 1, 1)) return cudaErrorNotSupported;
+    static std::atomic<uint64_t> attr{0};
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(paged_chunk_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 Geo<HD>::SMEM);
+        e = smem_limit(reinterpret_cast<const void*>(paged_chunk_kernel<HD>), Geo<HD>::SMEM, attr);
     if (e != cudaSuccess) return e;
     const int grid = min(sms, MAX_CTAS);
     PagedDesc* desc = static_cast<PagedDesc*>(a.ws);
@@ -647,8 +743,9 @@ size_t paged_chunk_workspace(int hd) {
     return MAX_CTAS * (sizeof(PagedDesc) + 2 * p);
 }
 
-cudaError_t launch_paged_chunk(const PagedArgs& a, cudaStream_t st) {
+cudaError_t launch_paged_chunk(PagedArgs a, cudaStream_t st) {
     if (a.n_tokens <= 0 || a.n_rows <= 0) return cudaSuccess;
+    a.line_heads = a.Hkv;
     return a.hd == 128 ? launch_chunk<128>(a, st) : launch_chunk<64>(a, st);
 }
 

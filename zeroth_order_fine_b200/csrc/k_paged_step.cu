@@ -5,8 +5,10 @@
 // HBM bounds it and the products only have to keep out of the way.  That decides the form:
 //
 // * The work of a call is one line of units -- 16 keys (with their values) of one (request, tile
-//   of query rows, kv head) -- and every warp of the grid takes an equal stretch of that line,
-//   whatever lengths the requests have.  A warp works alone: its own ring of shared-memory
+//   of query rows, team of kv heads) -- and every team of warps takes an equal stretch of that
+//   line, whatever lengths the requests have.  A team has a warp per head, gcd(Hkv, 8) of them,
+//   so its warps read neighbouring columns of the same cache rows at about the same time: whole
+//   rows come from HBM together.  A warp works alone: its own ring of shared-memory
 //   stages, its own barriers, running maxima, sums and outputs, no block-wide synchronisation.
 //   An item cut by a stretch's end is written as a partial (m, l, o) and the pieces are added in
 //   key order by a small second kernel.
@@ -105,18 +107,20 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// Slots of partial results, in the accumulator's own layout: slot 2 w: the piece with which worker
-// w's stretch begins (an item begun by an earlier worker); 2 w + 1: the one it ends with (an item
-// that goes on).  desc[w] describes the item of slot 2 w + 1.
+// Slots of partial results, in the accumulator's own layout: slot 2 w: the piece with which team
+// w's stretch begins (an item begun by an earlier team); 2 w + 1: the one it ends with (an item
+// that goes on); each with a part per warp of the team.  desc[w] describes the item of slot
+// 2 w + 1.
 template <int HD, int NB>
 struct Part {
     float4 o[HD / 16][NB][32];
     float m[NB * 8], l[NB * 8];
 };
 
-template <int HD, int NB>
+// 16-dim tiles mt0 .. mt0 + MT - 1 of the rows
+template <int HD, int NB, int MT>
 __device__ __forceinline__ void store_rows(const PagedArgs& a, int start, int row0, int rows, int kvh,
-                                           const float (*o)[NB][4], const float (*inv)[2], int lane) {
+                                           int mt0, const float (*o)[NB][4], const float (*inv)[2], int lane) {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -126,9 +130,9 @@ __device__ __forceinline__ void store_rows(const PagedArgs& a, int start, int ro
             const int row = row0 + n;
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
                                  (size_t)(start + row / a.g) * a.ld_out +
-                                 (size_t)(kvh * a.g + row % a.g) * HD + (lane >> 2);
+                                 (size_t)(kvh * a.g + row % a.g) * HD + mt0 * 16 + (lane >> 2);
 #pragma unroll
-            for (int mt = 0; mt < HD / 16; ++mt) {
+            for (int mt = 0; mt < MT; ++mt) {
                 out[mt * 16] = __float2bfloat16_rn(o[mt][nb][e] * inv[nb][e]);
                 out[mt * 16 + 8] = __float2bfloat16_rn(o[mt][nb][2 + e] * inv[nb][e]);
             }
@@ -156,10 +160,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     using Line = PagedLine<false, RB, UK>;
     const long long L = Line::prefix(a, GROUPS, cum, wsum);
-    const int workers = gridDim.x * WARPS, w = blockIdx.x * WARPS + warp;
+    const int team = min(WARPS, a.Hkv & -a.Hkv);      // a power of two, as WARPS is
+    const int workers = gridDim.x * (WARPS / team), w = blockIdx.x * (WARPS / team) + warp / team;
+    const int mate = warp % team;                     // the warp's head within the team's
     const long long stretch = (L + workers - 1) / workers;      // units per worker
     const long long u0 = stretch * w, u1 = min(L, u0 + stretch);
-    if (lane == 0) desc[w].pieces = 0;
+    if (mate == 0 && lane == 0) desc[w].pieces = 0;
     if (u0 >= u1) return;                             // nothing to do, nothing in flight
 
     typename Line::Cursor con = Line::locate(a, GROUPS, cum, u0);
@@ -211,7 +217,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
                         " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst + (uint32_t)(s * box_rows * HD * 4)),
                         "l"(reinterpret_cast<uint64_t>(&map)), "r"(bar), "r"(0), "r"(row[s]),
-                        "r"(pro.head * NH), "r"(0)
+                        "r"((pro.head * team + mate) * NH), "r"(0)
                         : "memory");
         }
     };
@@ -253,7 +259,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int rr = live ? row : row0;
                 const uint32_t* q = reinterpret_cast<const uint32_t*>(
                     static_cast<const __nv_bfloat16*>(a.q) + (size_t)(con.q.start + rr / a.g) * a.ld_q +
-                    (size_t)(con.head * a.g + rr % a.g) * HD + 2 * (lane & 3));
+                    (size_t)((con.head * team + mate) * a.g + rr % a.g) * HD + 2 * (lane & 3));
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk) {
                     qf[kk][nb][0] = live ? __ldg(q + kk * 8) : 0u;
@@ -377,9 +383,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) inv[nb][e] = 1.f / l[nb][e];
-                store_rows<HD, NB>(a, con.q.start, row0, rows, con.head, o, inv, lane);
+                store_rows<HD, NB, HD / 16>(a, con.q.start, row0, rows, con.head * team + mate, 0, o, inv, lane);
             } else {
-                Part<HD, NB>& p = part[2 * w + (first_unit == 0 ? 1 : 0)];
+                Part<HD, NB>& p = part[(2 * w + (first_unit == 0 ? 1 : 0)) * team + mate];
 #pragma unroll
                 for (int mt = 0; mt < HD / 16; ++mt)
 #pragma unroll
@@ -393,7 +399,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             p.m[nb * 8 + 2 * lane + e] = m[nb][e];
                             p.l[nb * 8 + 2 * lane + e] = l[nb][e];
                         }
-                if (first_unit == 0 && lane == 0) {
+                if (first_unit == 0 && mate == 0 && lane == 0) {
                     // the item's last unit is (units - 1) behind its first, which is u - unit
                     const long long last = u - con.unit + con.units - 1;
                     PagedDesc d;
@@ -401,7 +407,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     d.start = con.q.start;
                     d.row0 = row0;
                     d.rows = rows;
-                    d.kvh = con.head;
+                    d.kvh = con.head * team;
                     desc[w] = d;
                 }
             }
@@ -419,67 +425,89 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
-// Adds the pieces of the item that worker w's stretch ended inside, in key order: one warp per
-// worker, in the partials' own layout.
+// Adds the pieces of the item that team blockIdx.x's stretch ended inside, in key order, in the
+// partials' own layout, one CTA per head of the team: each warp takes a quarter of the dims.  The statistics of up to JOIN
+// pieces are fetched by all threads at once and the outputs of several pieces are in flight
+// together, so that the chain of dependent loads does not grow with the pieces.
+constexpr int JOIN = 32;
 template <int HD, int NB>
 __global__ void __launch_bounds__(128) paged_step_join_kernel(PagedArgs a, const PagedDesc* __restrict__ desc,
-                                                              const Part<HD, NB>* __restrict__ part,
-                                                              int workers) {
+                                                              const Part<HD, NB>* __restrict__ part) {
+    constexpr int MT = HD / 64;                       // 16-dim tiles of a warp
+    __shared__ float sm[JOIN][NB * 8], sl[JOIN][NB * 8];
     grid_dep_wait();
-    const int w = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (w >= workers) return;
+    const int w = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const PagedDesc d = desc[w];
     if (d.pieces <= 0) return;
     const float sl2 = a.scale * 1.4426950408889634f;
-    float o[HD / 16][NB][4], m[NB][2], l[NB][2];
     const int c = 2 * (lane & 3);
+    float o[MT][NB][4], m[NB][2], l[NB][2];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+    for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             m[nb][e] = -FLT_MAX;
             l[nb][e] = 0.f;
         }
-    for (int i = 0; i < d.pieces; ++i) {
-        const Part<HD, NB>& p = part[2 * (w + i) + (i == 0 ? 1 : 0)];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) m[nb][e] = fmaxf(m[nb][e], p.m[nb * 8 + c + e]);
-    }
-#pragma unroll
-    for (int mt = 0; mt < HD / 16; ++mt)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[mt][nb][e] = 0.f;
-    for (int i = 0; i < d.pieces; ++i) {
-        const Part<HD, NB>& p = part[2 * (w + i) + (i == 0 ? 1 : 0)];
-        float f[NB][2];
+    }
+    for (int i0 = 0; i0 < d.pieces; i0 += JOIN) {
+        const int n = min(JOIN, d.pieces - i0);
+        auto piece = [&](int i) {
+            return part + (size_t)(2 * (w + i0 + i) + (i0 + i == 0 ? 1 : 0)) * gridDim.y + blockIdx.y;
+        };
+        __syncthreads();
+        for (int i = threadIdx.x; i < n * NB * 8; i += 128) {
+            sm[i / (NB * 8)][i % (NB * 8)] = piece(i / (NB * 8))->m[i % (NB * 8)];
+            sl[i / (NB * 8)][i % (NB * 8)] = piece(i / (NB * 8))->l[i % (NB * 8)];
+        }
+        __syncthreads();
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                f[nb][e] = ex2((p.m[nb * 8 + c + e] - m[nb][e]) * sl2);
-                l[nb][e] += f[nb][e] * p.l[nb * 8 + c + e];
-            }
+                float mn = m[nb][e];
+                for (int i = 0; i < n; ++i) mn = fmaxf(mn, sm[i][nb * 8 + c + e]);
+                const float f = ex2((m[nb][e] - mn) * sl2);
+                l[nb][e] *= f;
 #pragma unroll
-        for (int mt = 0; mt < HD / 16; ++mt)
+                for (int mt = 0; mt < MT; ++mt) {
+                    o[mt][nb][e] *= f;
+                    o[mt][nb][e + 2] *= f;
+                }
+                m[nb][e] = mn;
+            }
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const Part<HD, NB>* p = piece(i);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-                const float4 v = p.o[mt][nb][lane];
-                o[mt][nb][0] = fmaf(f[nb][0], v.x, o[mt][nb][0]);
-                o[mt][nb][1] = fmaf(f[nb][1], v.y, o[mt][nb][1]);
-                o[mt][nb][2] = fmaf(f[nb][0], v.z, o[mt][nb][2]);
-                o[mt][nb][3] = fmaf(f[nb][1], v.w, o[mt][nb][3]);
+                float f[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    f[e] = ex2((sm[i][nb * 8 + c + e] - m[nb][e]) * sl2);
+                    l[nb][e] = fmaf(f[e], sl[i][nb * 8 + c + e], l[nb][e]);
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const float4 v = p->o[warp * MT + mt][nb][lane];
+                    o[mt][nb][0] = fmaf(f[0], v.x, o[mt][nb][0]);
+                    o[mt][nb][1] = fmaf(f[1], v.y, o[mt][nb][1]);
+                    o[mt][nb][2] = fmaf(f[0], v.z, o[mt][nb][2]);
+                    o[mt][nb][3] = fmaf(f[1], v.w, o[mt][nb][3]);
+                }
             }
+        }
     }
     float inv[NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int e = 0; e < 2; ++e) inv[nb][e] = 1.f / l[nb][e];
-    store_rows<HD, NB>(a, d.start, d.row0, d.rows, d.kvh, o, inv, lane);
+    store_rows<HD, NB, MT>(a, d.start, d.row0, d.rows, d.kvh + blockIdx.y, warp * MT, o, inv, lane);
 }
 
 template <int HD, int NB>
@@ -487,22 +515,21 @@ cudaError_t launch_step(const PagedArgs& a, cudaStream_t st) {
     CUtensorMap map;
     const int box_rows = min(UK, 1 << a.page_shift);
     if (!paged_cache_map(&map, a, box_rows, HD / 64, 2)) return cudaErrorNotSupported;
+    static std::atomic<uint64_t> attr{0};
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(paged_step_kernel<HD, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 Geo<HD>::SMEM);
+        e = smem_limit(reinterpret_cast<const void*>(paged_step_kernel<HD, NB>), Geo<HD>::SMEM, attr);
     if (e != cudaSuccess) return e;
-    const int grid = min(sms, MAX_CTAS);
+    const int grid = min(sms, MAX_CTAS), team = min(WARPS, a.Hkv & -a.Hkv);
     PagedDesc* desc = static_cast<PagedDesc*>(a.ws);
     auto* part = reinterpret_cast<Part<HD, NB>*>(static_cast<char*>(a.ws) + MAX_WORKERS * sizeof(PagedDesc));
     paged_step_kernel<HD, NB><<<grid, THREADS, Geo<HD>::SMEM, st>>>(map, a, box_rows, desc, part);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int workers = grid * WARPS;
-    return launch_pdl(paged_step_join_kernel<HD, NB>, dim3((workers + 3) / 4), dim3(128), 0, st, a,
-                      static_cast<const PagedDesc*>(desc), static_cast<const Part<HD, NB>*>(part), workers);
+    return launch_pdl(paged_step_join_kernel<HD, NB>, dim3(grid * (WARPS / team), team), dim3(128), 0, st, a,
+                      static_cast<const PagedDesc*>(desc), static_cast<const Part<HD, NB>*>(part));
 }
 
 }  // namespace
@@ -519,8 +546,9 @@ bool paged_tc_supported(const PagedArgs& a) {
            a.ld_q % 8 == 0 && a.ld_out % 8 == 0;
 }
 
-cudaError_t launch_paged_step(const PagedArgs& a, cudaStream_t st) {
+cudaError_t launch_paged_step(PagedArgs a, cudaStream_t st) {
     if (a.n_tokens <= 0 || a.n_rows <= 0) return cudaSuccess;
+    a.line_heads = a.Hkv / min(WARPS, a.Hkv & -a.Hkv);
     const bool one = (long long)a.max_new * a.g <= 8;
     if (a.hd == 128) return one ? launch_step<128, 1>(a, st) : launch_step<128, 2>(a, st);
     return one ? launch_step<64, 1>(a, st) : launch_step<64, 2>(a, st);

@@ -211,15 +211,16 @@ struct PagedArgs {
     int dtype;
     void* out; long long ld_out;
     void* ws;
+    int line_heads;                         // groups of kv heads on a kernel's line of work
     int step_tokens;                        // requests of at most so many new tokens take the
                                             // decode-step kernel
 };
 cudaError_t launch_paged_attention(const PagedArgs& a, cudaStream_t st);   // CUDA cores
 bool paged_tc_supported(const PagedArgs& a);                               // bf16, head_dim 64 or 128
-cudaError_t launch_paged_step(const PagedArgs& a, cudaStream_t st);
+cudaError_t launch_paged_step(PagedArgs a, cudaStream_t st);
 size_t paged_step_workspace(int hd);
 int paged_step_error_word();
-cudaError_t launch_paged_chunk(const PagedArgs& a, cudaStream_t st);       // the other requests
+cudaError_t launch_paged_chunk(PagedArgs a, cudaStream_t st);       // the other requests
 size_t paged_chunk_workspace(int hd);
 int paged_chunk_error_word();
 

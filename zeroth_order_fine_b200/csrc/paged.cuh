@@ -11,14 +11,15 @@ namespace zo {
 
 // A kernel takes the requests of at most step_tokens new tokens (BIG false) or the others (BIG
 // true); the rest have no rows for it.  RB query rows (new tokens x g of one kv head) make a tile,
-// UK keys a unit.
+// UK keys a unit; a place on the line stands for line_heads-th parts of the kv heads.
 template <bool BIG, int RB, int UK>
 struct PagedLine {
     struct Req {
         int start, rows, ctx;             // first packed row, rows per kv head, tokens before
         bool bad;                         // the length cannot be used: NaN rows
     };
-    // a place on the line: units of a (request, tile, kv head) in key order, heads, tiles, requests
+    // a place on the line: units of a (request, tile, group of kv heads) in key order, then groups
+    // (line_heads of them), tiles, requests
     struct Cursor {
         Req q;
         int r, tile, head, unit, units;
@@ -45,7 +46,7 @@ struct PagedLine {
         const Req q = get(a, r);
         long long u = 0;
         for (int t = 0; t * RB < q.rows; ++t) u += units(a, q, t);
-        return u * a.Hkv;
+        return u * a.line_heads;
     }
     // Prefix sums of the requests' units in groups of ceil(n_rows / max_groups) requests: cum[0 ..
     // groups]; every thread of the block takes part and gets the total.  wsum: one per warp.
@@ -104,7 +105,7 @@ struct PagedLine {
         k.tile = 0;
         for (;;) {
             k.units = units(a, k.q, k.tile);
-            const long long n = (long long)k.units * a.Hkv;
+            const long long n = (long long)k.units * a.line_heads;
             if (rest < n) break;
             rest -= n;
             ++k.tile;
@@ -119,7 +120,7 @@ struct PagedLine {
         k.unit += n;
         if (k.unit < k.units) return;
         k.unit = 0;
-        if (++k.head < a.Hkv) return;
+        if (++k.head < a.line_heads) return;
         k.head = 0;
         if (!more) return;
         if (++k.tile * RB >= k.q.rows) {
