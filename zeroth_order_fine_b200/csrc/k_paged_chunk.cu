@@ -163,13 +163,22 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
         "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
         : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-        "%14,%15,%16};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t* v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]),
+                   "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]),
+                   "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :
+                 : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -485,36 +494,51 @@ __global__ void __launch_bounds__(THREADS, 1)
             // keys below lim are seen by this row
             const int lim = it.q.bad || !live ? 0 : it.q.ctx + r / a.g + 1;
             const int e = p.end(t);
+            const uint64_t c2 = pair(sl2, sl2);
             for (int c = p.c0; c < e; ++c) {
                 if (!wait_bar(s_full(t), ns & 1, abort_f)) { ok = false; break; }
                 ++ns;
                 fence_after();
                 bad |= bad_unit[(unit + c - p.c0) & 7] != 0;
-                // The row is read twice, 32 scores at a time with the next 32 on their way: once for
-                // the maximum, once for the exponentials.  Held at once it does not fit beside
-                // the rest (128 scores spilled).
+                // One pass over the row's scores, 16 at a time with the next 16 on their way: the
+                // exponentials are taken against the reference as it stands while the maximum is
+                // looked for.  Only when the maximum turns out to be over 2^8 above the reference
+                // (a piece's first unit, rarely later) does it move, and the pass is repeated; the
+                // scores are still there, since P goes out at the end.
                 const int cut = lim - c * UK;
                 const bool masked = !__all_sync(0xffffffffu, cut >= UK);
-                uint32_t sv[2][32];
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                tmem_ld32(ts, sv[0]);
+                uint32_t pk[64];
+                uint64_t ln[4];
+                for (;;) {
+                    const uint64_t m2 = pair(-m, -m);
+                    uint32_t sv[2][16];
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t* v = sv[h & 1];
-                    tmem_wait_ld(v);
-                    tmem_ld32(ts + ((h + 1) & 3) * 32, sv[(h + 1) & 1]);
-                    if (masked) {
+                    for (int i = 0; i < 4; ++i) ln[i] = l[i];
+                    tmem_ld16(ts, sv[0]);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (h * 32 + j >= cut) v[j] = __float_as_uint(-INFINITY);
+                    for (int h = 0; h < 8; ++h) {
+                        uint32_t* v = sv[h & 1];
+                        tmem_wait_ld16(v);
+                        if (h < 7) tmem_ld16(ts + (h + 1) * 16, sv[(h + 1) & 1]);
+                        if (masked) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                if (h * 16 + j >= cut) v[j] = __float_as_uint(-INFINITY);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const float s0 = __uint_as_float(v[j]), s1 = __uint_as_float(v[j + 1]);
+                            mx[(j >> 1) & 3] = fmaxf(mx[(j >> 1) & 3], fmaxf(s0, s1));
+                            const float2 x = unpair(fma2(pair(s0, s1), c2, m2));
+                            const float p0 = ex2(x.x), p1 = ex2(x.y);
+                            ln[(j >> 1) & 3] = add2(ln[(j >> 1) & 3], pair(p0, p1));
+                            pk[h * 8 + j / 2] = pack2(p0, p1);
+                        }
                     }
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(v[j]));
-                }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-                // the reference moves when the maximum is over 2^8 above it (at first, at once)
-                const bool move = top > m + 8.f;
-                if (__any_sync(0xffffffffu, move)) {
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+                    const bool move = top > m + 8.f;
+                    if (!__any_sync(0xffffffffu, move)) break;
                     const float mn = move ? top : m;
                     const float f = ex2(m - mn);      // 1 where it stays; 0 from the start value
                     if (c > p.c0) {
@@ -523,7 +547,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int j = 0; j < HD / 32; ++j) {
                             uint32_t v[32];
                             tmem_ld32(to + j * 32, v);
-                            tmem_wait_ld(v);          // (and for the scores on their way)
+                            tmem_wait_ld(v);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
                             tmem_st32(to + j * 32, v);
@@ -534,28 +558,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int i = 0; i < 4; ++i) l[i] = fma2(l[i], f2, 0ull);
                     m = mn;
                 }
-                const uint64_t c2 = pair(sl2, sl2), m2 = pair(-m, -m);
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t* v = sv[h & 1];
-                    tmem_wait_ld(v);
-                    if (h < 3) tmem_ld32(ts + (h + 1) * 32, sv[(h + 1) & 1]);
-                    if (masked) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (h * 32 + j >= cut) v[j] = __float_as_uint(-INFINITY);
-                    }
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float2 x = unpair(fma2(pair(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), c2, m2));
-                        const float p0 = ex2(x.x), p1 = ex2(x.y);
-                        l[(j >> 1) & 3] = add2(l[(j >> 1) & 3], pair(p0, p1));
-                        pk[j / 2] = pack2(p0, p1);
-                    }
-                    // over scores that have been read: columns 16 h .. of 32 h ..
-                    tmem_st16(ts + h * 16, pk);
-                }
+                for (int i = 0; i < 4; ++i) l[i] = ln[i];
+                tmem_st32(ts, pk);
+                tmem_st32(ts + 32, pk + 32);
                 tmem_wait_st();
                 const int valid = p.valid(c);
                 if (valid < UK && (valid & 15)) {
