@@ -76,6 +76,21 @@ inline cudaError_t smem_limit(const void* kernel, int bytes, std::atomic<uint64_
     return e;
 }
 
+// Asks for the largest shared memory share of the L1 for a small kernel, once per device: an SM
+// changes the split only when it is idle, so a kernel that needs most of it (the GEMMs) can start
+// beside this one only if this one runs with that split already.
+inline cudaError_t smem_share(const void* kernel, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
 // ---- debug build (ZO_DEBUG): device bounds checks -------------------------------------
 // ZO_DCHECK(cond, bit) is `cond` in the debug build, where a failed check also ORs `bit` into
 // the translation unit's debug word and the caller skips the access; in the release build it

@@ -1,21 +1,21 @@
 // One linear layer for rows of many requests, each row under an adapter of its own:
 //   y[m] = act(x[m] W^T + b + scale[a] (x[m] A_a^T) B_a^T),  a = row_adapter[m].
 //
-// Tensor-core forms (bf16).  Which one: DIRECT below.
-//   direct: few output tiles (decode steps, M <= 128 rows always), where the product is a stream
-//     of W over split K slices: the rows' shrink S in fp32 runs beside it on CUDA cores, and the
-//     slices' reduction adds S[m] B_a^T from the row's own factors before bias and activation.
-//   tiles: the expand runs as extra K blocks of the product's tcgen05 GEMM (S masked per row,
-//     zeros for other adapters), each 256-row block with only the 64-column blocks of B that its
-//     rows' adapters touch, and of those only the 16-column steps.
+// Tensor-core forms (bf16): the expand runs as extra K blocks of the product's tcgen05 GEMM, with the
+// rows' shrink S masked to their own adapter (zeros in the others' columns); of the factors' 64-column
+// blocks, and of those the 16-column steps, only those that the rows at hand touch.
+//   decode steps (up to 128 rows): the product is a stream of W, the weights on the tensor cores'
+//     128-row side; S comes from a CUDA-core kernel beside its first blocks.
+//   more rows: per 256-row block a list of blocks, S from a tcgen05 shrink, 256 x 256 output tiles.
+// An output that the zeros have made non-finite (0 times another adapter's infinity) is computed anew
+// from the row's own factors.
 //
 // CUDA-core form (fp32, and shapes the tensor cores do not take): the rows' shrink
 // S[m, j] = scale[a] x[m] . A_a[j] goes to the workspace in fp32, then a tiled GEMM adds
 // S[m] B_a^T to each of its tiles before the bias, activation and rounding.
 #include <cstring>
 
-#include "common.cuh"
-#include "kernels.h"
+#include "adapters.cuh"
 
 namespace zo {
 
@@ -111,152 +111,133 @@ __global__ void __launch_bounds__(256) adapter_gemm_kernel(AdapterArgs a, const 
 
 // ---- tensor-core forms ----------------------------------------------------------------------
 
-__device__ __forceinline__ void bf8(const uint4& u, float* f) {
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 t = __bfloat1622float2(h[i]);
-        f[2 * i] = t.x;
-        f[2 * i + 1] = t.y;
-    }
-}
-
-// The fp32 shrink of the rows' own adapters (direct form): one warp per (m, j), 16-byte loads;
-// the warps of a CTA share row m through L1.  The CTAs behind those (FETCH_CTAS of them) ask L2 for
-// the rows' expand factors, output row by output row, while the product streams W: the reduction
-// reads them in 2 rank-byte pieces, which from HBM, each by itself, took it 15 us instead of 6 (48
-// rows, 32 adapters of rank 16, OPT-13B q|k|v).
-constexpr int FETCH_CTAS = 148;
-__global__ void __launch_bounds__(SH_WARPS * 32) adapter_shrink_rows_kernel(AdapterArgs a, float* S) {
-    grid_dep_launch();                 // the product does not read S: it may start now
-    const int lane = threadIdx.x & 31, groups = (a.rank + SH_WARPS - 1) / SH_WARPS;
-    const int fetch = (int)blockIdx.x - a.M * groups;
-    if (fetch >= 0) {
-        const size_t ldb = (size_t)a.n_adapters * a.rank * 2;
-        for (int m0 = 0; m0 < a.M; m0 += 32) {
-            const int id = m0 + lane < a.M ? a.ids[m0 + lane] : -1;
-            // one lane per adapter of these rows
-            const unsigned same = __match_any_sync(0xffffffffu, id);
-            if (id < 0 || id >= a.n_adapters || (same & ((1u << lane) - 1u))) continue;
-            const char* b = static_cast<const char*>(a.B) + (size_t)id * a.rank * 2;
-            for (int n = fetch * SH_WARPS + (threadIdx.x >> 5); n < a.N; n += FETCH_CTAS * SH_WARPS)
-                for (int c = 0; c < a.rank * 2; c += 32)
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(b + (size_t)n * ldb + c));
-        }
-        return;
-    }
-    const int m = (int)blockIdx.x / groups;
-    const int j = (int)blockIdx.x % groups * SH_WARPS + (threadIdx.x >> 5);
+// The rows' shrink for the decode form: S[m, j] = scale[a] x[m] . A_a[j] in fp32, rounded to bf16
+// into row m of the masked S (the products' extension operand), whose other columns become zeros in
+// the blocks that any row uses.  A warp takes JW of the adapter's rows, so that x[m] is read once for
+// them; 16-byte loads; the warps of a CTA share row m through L1.  The first CTA also writes the list
+// of blocks: those that the rows' adapters touch, with the mask of their 16-column steps.
+template <int JW>
+__global__ void __launch_bounds__(SH_WARPS * 32)
+    adapter_shrink_rows_kernel(AdapterArgs a, __nv_bfloat16* __restrict__ S, int ldS, int* __restrict__ cnt,
+                               int* __restrict__ list) {
+    __shared__ unsigned steps[4096 / 32];      // one bit per 16-column step of 65536 columns
+    grid_dep_launch();                         // the product reads S and the list only at its end
+    const int groups = (a.rank + JW * SH_WARPS - 1) / (JW * SH_WARPS);
+    const int m = (int)blockIdx.x / groups, grp = (int)blockIdx.x % groups;
+    const int lane = threadIdx.x & 31, n_list = ldS / 64;
     const int id = a.ids[m];
-    if (id < 0 || id >= a.n_adapters || j >= a.rank) return;
-    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + (size_t)m * a.K);
-    const uint4* f = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.A) +
-                                                    ((size_t)id * a.rank + j) * a.K);
-    const int n8 = a.K / 8;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int k = lane; k < n8; k += 32) {
-        float xv[8], fv[8];
-        bf8(__ldg(x + k), xv);
-        bf8(__ldg(f + k), fv);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[i & 3] = fmaf(xv[i], fv[i], s[i & 3]);
+    const bool live = id >= 0 && id < a.n_adapters;
+    if (grp == 0) {
+        for (int i = threadIdx.x; i < (n_list + 7) / 8; i += blockDim.x) steps[i] = 0u;
+        __syncthreads();
+        if (threadIdx.x < a.M) {
+            const int r = a.ids[threadIdx.x];
+            if (r >= 0 && r < a.n_adapters)
+                for (int s = r * a.rank / 16; s <= ((r + 1) * a.rank - 1) / 16; ++s)
+                    atomicOr(&steps[s >> 5], 1u << (s & 31));
+        }
+        __syncthreads();
+        const int lo = live ? id * a.rank : 0, hi = live ? lo + a.rank : 0;
+        for (int b = threadIdx.x; b < n_list; b += blockDim.x) {
+            const int mask = (int)((steps[b >> 3] >> (4 * (b & 7))) & 15u);
+            if (!mask) continue;
+            for (int c = b * 64; c < b * 64 + 64; c += 8) {
+                __nv_bfloat16* p = S + (size_t)m * ldS + c;
+                if (c + 8 <= lo || c >= hi) {
+                    *reinterpret_cast<uint4*>(p) = make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                    for (int i = 0; i < 8; ++i)
+                        if (c + i < lo || c + i >= hi) p[i] = __float2bfloat16_rn(0.f);
+                }
+            }
+        }
+        if (m == 0 && threadIdx.x < 32) {              // the list, ascending
+            int used = 0;
+            for (int b0 = 0; b0 < n_list; b0 += 32) {
+                const int b = b0 + lane;
+                const int mask = b < n_list ? (int)((steps[b >> 3] >> (4 * (b & 7))) & 15u) : 0;
+                const unsigned have = __ballot_sync(0xffffffffu, mask != 0);
+                if (mask) list[used + __popc(have & ((1u << lane) - 1u))] = b | (mask << 16);
+                used += __popc(have);
+            }
+            if (lane == 0) *cnt = used;
+        }
     }
-    const float v = warp_sum((s[0] + s[1]) + (s[2] + s[3]));
-    if (lane == 0) S[(size_t)m * a.rank + j] = v * a.scale[id];
+    const int j0 = (grp * SH_WARPS + (int)(threadIdx.x >> 5)) * JW;
+    if (!live || j0 >= a.rank) return;
+    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + (size_t)m * a.K);
+    const uint4* f[JW];
+#pragma unroll
+    for (int q = 0; q < JW; ++q)
+        f[q] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.A) +
+                                              ((size_t)id * a.rank + min(j0 + q, a.rank - 1)) * a.K);
+    float s[JW][2];
+#pragma unroll
+    for (int q = 0; q < JW; ++q) s[q][0] = s[q][1] = 0.f;
+#pragma unroll 4
+    for (int k = lane; k < a.K / 8; k += 32) {
+        float xv[8];
+        bf8(__ldg(x + k), xv);
+#pragma unroll
+        for (int q = 0; q < JW; ++q) {
+            float fv[8];
+            bf8(__ldg(f[q] + k), fv);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[q][i & 1] = fmaf(xv[i], fv[i], s[q][i & 1]);
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < JW; ++q) {
+        const float v = warp_sum(s[q][0] + s[q][1]);
+        if (lane == 0 && j0 + q < a.rank)
+            S[(size_t)m * ldS + (size_t)id * a.rank + j0 + q] = __float2bfloat16_rn(v * a.scale[id]);
+    }
 }
 
-// Output of 4 columns n.. of row m from the product's sums y.
-__device__ __forceinline__ void adapter_store4(const AdapterArgs& a, int m, int n, const float* y) {
-    const size_t at = (size_t)m * a.N + n;
-    float v[4];
+template <int JW>
+cudaError_t launch_shrink_rows(const AdapterArgs& a, __nv_bfloat16* S, int ldS, int* cnt, int* list,
+                               cudaStream_t st) {
+    static std::atomic<uint64_t> share{0};
+    const cudaError_t e = smem_share(reinterpret_cast<const void*>(adapter_shrink_rows_kernel<JW>), share);
+    if (e != cudaSuccess) return e;
+    adapter_shrink_rows_kernel<JW>
+        <<<a.M * cdiv(a.rank, JW * SH_WARPS), SH_WARPS * 32, 0, st>>>(a, S, ldS, cnt, list);
+    return cudaGetLastError();
+}
+
+// The slices' reduction of the decode form: one thread per 4 columns of a row adds them in split
+// order, with bias and activation; sums that are not finite are taken anew from the row's own factors.
+__global__ void __launch_bounds__(128)
+    adapter_reduce_kernel(AdapterArgs a, const __nv_bfloat16* __restrict__ S, int ldS,
+                          const float* __restrict__ ws, int ks) {
+    const int m = blockIdx.y, n = (blockIdx.x * blockDim.x + threadIdx.x) * 4;
+    const int id = a.ids[m];
+    grid_dep_wait();
+    if (n >= a.N) return;
+    float y[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < ks; ++k) {
+        const float4 w = *reinterpret_cast<const float4*>(ws + ((size_t)k * a.M + m) * a.N + n);
+        y[0] += w.x; y[1] += w.y; y[2] += w.z; y[3] += w.w;
+    }
+    const bool none = id < -1 || id >= a.n_adapters;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        v[i] = y[i] + (a.bias ? a.bias[n + i] : 0.f);
-        if (a.act == 1) v[i] = v[i] < 0.f ? 0.f : v[i];       // a NaN stays
+        if (none) y[i] = __int_as_float(0x7fc00000);
+        else if (!isfinite(y[i])) y[i] = adapter_element(a, S, ldS, m, n + i, id, 0, 1);
+        if (a.bias) y[i] += a.bias[n + i];
+        if (a.act == 1) y[i] = y[i] < 0.f ? 0.f : y[i];       // a NaN stays
     }
+    const size_t at = (size_t)m * a.N + n;
     if (a.accumulate) {
         float4* c = reinterpret_cast<float4*>(static_cast<float*>(a.y) + at);
         float4 o = *c;
-        o.x += v[0]; o.y += v[1]; o.z += v[2]; o.w += v[3];
+        o.x += y[0]; o.y += y[1]; o.z += y[2]; o.w += y[3];
         *c = o;
     } else {
-        __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+        __nv_bfloat162 lo = __floats2bfloat162_rn(y[0], y[1]), hi = __floats2bfloat162_rn(y[2], y[3]);
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.y) + at) =
             make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
     }
-}
-
-// The slices' reduction of the direct form: a CTA takes 512 columns of a row.  First the expand
-// S[m] B_a[n]^T of its columns into shared memory: LPR lanes share a row of B (LPR 16-byte loads side
-// by side, so that a warp's load takes whole sectors), their sums joined by shuffles.  Then
-// each thread adds the slices of 4 columns in split order, the expand, bias and activation.
-template <int LPR>
-__device__ __forceinline__ void adapter_expand(const AdapterArgs& a, const float* __restrict__ s,
-                                               const __nv_bfloat16* __restrict__ b, size_t ldb, int n0,
-                                               int n1, float* e) {
-    constexpr int ROWS = 32 / LPR;            // rows of B per warp and load
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = lane % LPR;
-#pragma unroll 4
-    for (int i = 0; i < 128; i += ROWS) {
-        const int n = n0 + warp * 128 + i + lane / LPR;
-        float y = 0.f;
-        if (n < n1)
-            for (int c = part * 8; c < a.rank; c += LPR * 8) {
-                float bv[8];
-                bf8(__ldg(reinterpret_cast<const uint4*>(b + n * ldb + c)), bv);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) y = fmaf(s[c + q], bv[q], y);
-            }
-#pragma unroll
-        for (int d = LPR / 2; d > 0; d >>= 1) y += __shfl_xor_sync(0xffffffffu, y, d);
-        if (part == 0) e[warp * 128 + i + lane / LPR] = y;
-    }
-}
-
-__global__ void __launch_bounds__(128)
-    adapter_reduce_kernel(AdapterArgs a, const float* __restrict__ S, const float* __restrict__ ws, int ks) {
-    __shared__ __align__(16) float e[512];
-    __shared__ float s[256];
-    const int m = blockIdx.y, n0 = blockIdx.x * 512, n = n0 + threadIdx.x * 4;
-    const int id = a.ids[m];
-    const bool live = id >= 0 && id < a.n_adapters;
-    grid_dep_wait();
-    float y[4] = {0.f, 0.f, 0.f, 0.f};
-    if (n < a.N)
-        for (int k = 0; k < ks; ++k) {
-            const float4 w = *reinterpret_cast<const float4*>(ws + ((size_t)k * a.M + m) * a.N + n);
-            y[0] += w.x; y[1] += w.y; y[2] += w.z; y[3] += w.w;
-        }
-    if (live) {
-        for (int c = threadIdx.x; c < a.rank; c += 128) s[c] = S[(size_t)m * a.rank + c];
-        __syncthreads();
-        const size_t ldb = (size_t)a.n_adapters * a.rank;
-        const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(a.B) + (size_t)id * a.rank;
-        const int n1 = min(a.N, n0 + 512);
-        if (a.rank % 64 == 0) {
-            adapter_expand<8>(a, s, b, ldb, n0, n1, e);
-        } else if (a.rank % 16 == 0) {
-            adapter_expand<2>(a, s, b, ldb, n0, n1, e);
-        } else if (a.rank % 8 == 0) {
-            adapter_expand<1>(a, s, b, ldb, n0, n1, e);
-        } else {
-            for (int i = threadIdx.x; n0 + i < n1; i += 128) {
-                float v = 0.f;
-                for (int c = 0; c < a.rank; ++c) v = fmaf(s[c], __bfloat162float(b[(n0 + i) * ldb + c]), v);
-                e[i] = v;
-            }
-        }
-        __syncthreads();
-        if (n < a.N) {
-            const float4 v = *reinterpret_cast<const float4*>(e + threadIdx.x * 4);
-            y[0] += v.x; y[1] += v.y; y[2] += v.z; y[3] += v.w;
-        }
-    } else if (id != -1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = __int_as_float(0x7fc00000);
-    }
-    if (n < a.N) adapter_store4(a, m, n, y);
 }
 
 // The tiles form's lists: CTA = a block of 256 rows, thread = a row.  A block's list holds the
@@ -326,48 +307,19 @@ __global__ void __launch_bounds__(FIX_THREADS)
             float mine = __int_as_float(0x7fc00000);
             if (!bad)
                 for (int j = 0; j < 32 && c * 32 + j < a.N; ++j) {
-                    const int n = c * 32 + j;
-                    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + (size_t)m * a.K);
-                    const uint4* w = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.W) + (size_t)n * a.K);
-                    float v = 0.f;
-                    for (int k = lane; k < a.K / 8; k += 32) {
-                        float xv[8], wv[8];
-                        bf8(__ldg(x + k), xv);
-                        bf8(__ldg(w + k), wv);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v = fmaf(xv[i], wv[i], v);
-                    }
-                    if (id >= 0) {
-                        const size_t col = (size_t)id * a.rank;
-                        const size_t ldb = (size_t)a.n_adapters * a.rank;
-                        for (int k = lane; k < a.rank; k += 32)
-                            v = fmaf(__bfloat162float(S[(size_t)m * ldS + col + k]),
-                                     __bfloat162float(static_cast<const __nv_bfloat16*>(a.B)[(size_t)n * ldb + col + k]), v);
-                    }
-                    v = warp_sum(v);
+                    const float v = warp_sum(adapter_element(a, S, ldS, m, c * 32 + j, id, lane, 32));
                     if (lane == j) mine = v;
                 }
-            const int n = c * 32 + lane;
-            if (n >= a.N) continue;
-            float v = mine + (a.bias ? a.bias[n] : 0.f);
-            if (a.act == 1) v = v < 0.f ? 0.f : v;
-            const size_t at = (size_t)m * a.N + n;
-            if (a.accumulate) static_cast<float*>(a.y)[at] += v;
-            else static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
+            if (c * 32 + lane < a.N) adapter_store(a, m, c * 32 + lane, mine);
         }
     }
 }
 
-// DIRECT: at most 128 rows, where the swapped single-SM product streams W, or too few 256 x 256
-// output tiles to give every SM pair two.
-bool direct_form(int M, int N) {
-    const long long tiles = (long long)((M + 255) / 256) * ((N + 255) / 256);
-    return M <= 128 || (N > 128 && tiles < 37);
-}
-
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Slices of the direct form: room for up to 16 splits, 64 MB at most unless one slice is more.
+constexpr int STEP_ROWS = 128;           // rows up to which the decode form is taken
+
+// Slices of the decode form: room for up to 16 splits, 64 MB at most unless one slice is more.
 size_t slice_floats(int M, int N) {
     const size_t one = (size_t)M * N;
     const size_t most = ((size_t)64 << 20) / 4 / one;
@@ -404,8 +356,8 @@ size_t adapter_workspace(int M, int N, int K, int n_adapters, int rank, int dtyp
     (void)K;
     const size_t s = up256((size_t)M * rank * 4) + 256;
     if (dtype != E_BF16 || M == 0) return s;
-    if (direct_form(M, N)) return s + up256(slice_floats(M, N) * 4);
-    const size_t t = tile_space(M, N, n_adapters * rank).total;
+    size_t t = tile_space(M, N, n_adapters * rank).total;
+    if (M <= STEP_ROWS) t += up256(slice_floats(M, N) * 4);
     return t > s ? t : s;
 }
 
@@ -416,11 +368,12 @@ cudaError_t launch_linear_adapters_simt(const AdapterArgs& a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_adapter_reduce(const AdapterArgs& a, const float* S, const float* ws, int ks,
+cudaError_t launch_adapter_reduce(const AdapterArgs& a, const AdapterTiles& t, const float* ws, int ks,
                                   cudaStream_t st, bool pdl) {
-    const dim3 grid(cdiv(a.N, 512), a.M);
-    if (pdl) return launch_pdl(adapter_reduce_kernel, grid, dim3(128), 0, st, a, S, ws, ks);
-    adapter_reduce_kernel<<<grid, 128, 0, st>>>(a, S, ws, ks);
+    const dim3 grid(cdiv(a.N / 4, 128), a.M);
+    const __nv_bfloat16* S = static_cast<const __nv_bfloat16*>(t.S);
+    if (pdl) return launch_pdl(adapter_reduce_kernel, grid, dim3(128), 0, st, a, S, t.ldS, ws, ks);
+    adapter_reduce_kernel<<<grid, 128, 0, st>>>(a, S, t.ldS, ws, ks);
     return cudaGetLastError();
 }
 
@@ -434,8 +387,18 @@ bool linear_adapters_tc_supported(const AdapterArgs& a) {
 
 cudaError_t launch_linear_adapters_tc(const AdapterArgs& a, cudaStream_t st) {
     char* ws = static_cast<char*>(a.ws);
-    if (direct_form(a.M, a.N)) {
-        float* S = reinterpret_cast<float*>(ws);
+    const int K2 = a.n_adapters * a.rank;
+    const TileSpace t = tile_space(a.M, a.N, K2);
+    AdapterTiles at;
+    int* cnt = reinterpret_cast<int*>(ws);
+    int* list = reinterpret_cast<int*>(ws + t.list);
+    at.cnt = cnt;
+    at.list = list;
+    at.n_list = t.n_list;
+    at.S = ws + t.s;
+    at.ldS = t.ld;
+    at.odd = reinterpret_cast<uint8_t*>(ws + t.odd);
+    if (a.M <= STEP_ROWS) {
         GemmArgs g;
         memset(&g, 0, sizeof(g));
         g.A = a.x; g.lda = a.K; g.a_type = E_BF16;
@@ -444,18 +407,18 @@ cudaError_t launch_linear_adapters_tc(const AdapterArgs& a, cudaStream_t st) {
         g.epi = a.accumulate ? EPI_RESID : a.act ? EPI_STORE_RELU : EPI_STORE;
         g.bias = a.bias;
         g.C = a.y; g.ldc = a.N; g.c_type = a.accumulate ? E_F32 : E_BF16;
-        g.ws = reinterpret_cast<float*>(ws + up256((size_t)a.M * a.rank * 4));
+        g.ws = reinterpret_cast<float*>(ws + t.total);
         g.ws_floats = slice_floats(a.M, a.N);
         g.adapt = &a;
-        g.adapt_S = S;
+        g.adapt_tiles = &at;
         if (!gemm_tc_supported(g)) return cudaErrorNotSupported;
-        adapter_shrink_rows_kernel<<<a.M * cdiv(a.rank, SH_WARPS) + FETCH_CTAS, SH_WARPS * 32, 0, st>>>(a, S);
-        cudaError_t e = cudaGetLastError();
+        __nv_bfloat16* S = static_cast<__nv_bfloat16*>(at.S);
+        // four of the adapter's rows per warp once that still fills the SMs
+        const cudaError_t e = a.M * a.rank >= 4 * 148 * SH_WARPS ? launch_shrink_rows<4>(a, S, t.ld, cnt, list, st)
+                                                                 : launch_shrink_rows<1>(a, S, t.ld, cnt, list, st);
         if (e != cudaSuccess) return e;
         return gemm_tc(g, st) ? cudaErrorUnknown : cudaSuccess;
     }
-    const int K2 = a.n_adapters * a.rank;
-    const TileSpace t = tile_space(a.M, a.N, K2);
     const int rows = pass_rows(a.M, K2);
     for (int m0 = 0; m0 < a.M; m0 += rows) {
         AdapterArgs b = a;
@@ -463,16 +426,7 @@ cudaError_t launch_linear_adapters_tc(const AdapterArgs& a, cudaStream_t st) {
         b.x = static_cast<const __nv_bfloat16*>(a.x) + (size_t)m0 * a.K;
         b.ids = a.ids + m0;
         b.y = static_cast<char*>(a.y) + (size_t)m0 * a.N * (a.accumulate ? 4 : 2);
-        AdapterTiles at;
-        at.cnt = reinterpret_cast<int*>(ws);
-        at.list = reinterpret_cast<int*>(ws + t.list);
-        at.n_list = t.n_list;
-        at.S = ws + t.s;
-        at.ldS = t.ld;
-        at.odd = reinterpret_cast<uint8_t*>(ws + t.odd);
-        adapter_lists_kernel<<<cdiv(b.M, 256), 256, 0, st>>>(b.ids, b.M, b.n_adapters, b.rank,
-                                                            const_cast<int*>(at.cnt), const_cast<int*>(at.list),
-                                                            at.n_list);
+        adapter_lists_kernel<<<cdiv(b.M, 256), 256, 0, st>>>(b.ids, b.M, b.n_adapters, b.rank, cnt, list, at.n_list);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         if (gemm_tc_adapters(b, at, st)) return cudaErrorUnknown;

@@ -28,6 +28,7 @@
 #include <algorithm>
 #include <cstring>
 
+#include "adapters.cuh"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -108,6 +109,8 @@ struct TcParams {
     uint8_t* odd;
     // the adapters' shrink: row ids, scales, rank
     const int* ids; const float* ad_scale; int n_adapters, ad_rank;
+    // decode steps under adapters: one split, so the kernel writes the output itself
+    AdapterArgs ad; const __nv_bfloat16* ad_S; int ad_ldS, final;
 };
 
 // ---- PTX wrappers ------------------------------------------------------------------
@@ -406,9 +409,21 @@ __device__ __forceinline__ void epilogue_swiglu(const TcParams& p, int m, int nb
     }
 }
 
+// 0 times every accumulator, summed: 0, or NaN if one of them is not finite
+template <int W>
+__device__ __forceinline__ float zero_times(const float* v) {
+    float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < W; ++j) z[j & 3] = fmaf(v[j], 0.f, z[j & 3]);
+    return (z[0] + z[1]) + (z[2] + z[3]);
+}
+
 // F8 (EPI_SPLIT_T only): the main K blocks are E4M3 (kind::f8f6f4, 128 elements per block),
 // the extension blocks bf16, into the same accumulator; the epilogue dequantises.
-template <int EPI, int BNT, bool F8 = false>
+// LIST (EPI_SPLIT_T only; adapters): the extension blocks are the listed ones, dealt to the splits
+// in turn; lists and S come from the kernel before, which is waited for only when the main blocks
+// are on their way.
+template <int EPI, int BNT, bool F8 = false, bool LIST = false>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmA2, const __grid_constant__ CUtensorMap tmB2,
@@ -477,7 +492,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         *kb0 = sp * p.kbs;
         *n_main = max(0, min(p.kbs, p.kb_main - *kb0));
-        *n_kb = *n_main + (sp == ks - 1 ? p.kb_ext : 0);
+        *n_kb = *n_main + (sp == ks - 1 && !LIST ? p.kb_ext : 0);
+    };
+    // (LIST) listed blocks of split sp: sp, sp + ks, ..
+    auto list_blocks = [&](int sp) {
+        grid_dep_wait();
+        return (p.cnt[0] - sp + ks - 1) / ks;
     };
 
     int n_armed = 0;                        // producer: loads issued; the i-th used stage i % S,
@@ -494,8 +514,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 tile_coords(t / ks, p, &mb, &nb);
                 int kb0, n_main, n_kb;
                 item_blocks(t % ks, &kb0, &n_main, &n_kb);
-                for (int i = 0; i < n_kb; ++i) {
-                    const int kb = i < n_main ? kb0 + i : p.kb_main + (i - n_main);
+                for (int i = 0; LIST || i < n_kb; ++i) {
+                    if (LIST && i == n_main) n_kb = n_main + list_blocks(t % ks);
+                    if (LIST && i >= n_kb) break;
+                    int kb = i < n_main ? kb0 + i : p.kb_main + (i - n_main);
+                    if (LIST && i >= n_main) kb = p.kb_main + (p.list[t % ks + (i - n_main) * ks] & 0xFFFF);
                     if (!mbar_wait(empty(s), ph ^ 1u, abort_f, p.err, p.wait_cycles)) { ok = false; break; }
                     const uint32_t sa = base + s * STAGE_BYTES;
                     const uint32_t sb = sa + A_BYTES;
@@ -527,7 +550,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const uint32_t d = tmem + (uint32_t)(acc * BNT);
                 int kb0, n_main, n_kb;
                 item_blocks(t % ks, &kb0, &n_main, &n_kb);
-                for (int i = 0; i < n_kb; ++i) {
+                for (int i = 0; LIST || i < n_kb; ++i) {
+                    if (LIST && i == n_main) n_kb = n_main + list_blocks(t % ks);
+                    if (LIST && i >= n_kb) break;
+                    const int steps = LIST && i >= n_main ? p.list[t % ks + (i - n_main) * ks] >> 16 : 0xF;
                     if (!mbar_wait(full(s), ph, abort_f, p.err, p.wait_cycles)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t sa = base + s * STAGE_BYTES;
@@ -540,8 +566,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     } else {
 #pragma unroll
                         for (int kk = 0; kk < BK / 16; ++kk) {
-                            tc_mma(d, sw128_desc(sa + kk * 32), sw128_desc(sb + kk * 32), T1::IDESC,
-                                   (i > 0 || kk > 0) ? 1u : 0u);
+                            if (!LIST || ((steps >> kk) & 1))
+                                tc_mma(d, sw128_desc(sa + kk * 32), sw128_desc(sb + kk * 32), T1::IDESC,
+                                       (i > 0 || kk > 0) ? 1u : 0u);
                         }
                     }
                     issued = true;
@@ -570,11 +597,50 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 // lane = feature m, columns = tokens: for each token the warp's 32 lanes
                 // write 32 consecutive features
                 float* slice = static_cast<float*>(p.C) + (size_t)(t % ks) * p.N * p.M;
+                if (LIST) grid_dep_wait();          // (S of the kernel before, should it be needed)
                 for (int c = 0; c < BNT / 32; ++c) {
                     const int n = nb * BNT + c * 32;
                     if (n >= p.N) break;            // warp-uniform
                     float v[32];
                     tmem_ld32(tmem + ((uint32_t)lane_base << 16) + (uint32_t)(acc * BNT + c * 32), v);
+                    if (LIST && p.final) {
+                        // the output itself: lane = feature, columns = tokens
+                        const int id_l = n + lane < p.N ? __ldg(p.ids + n + lane) : -1;
+                        const bool none = id_l < -1 || id_l >= p.n_adapters;
+                        const unsigned odd_ids = __ballot_sync(0xffffffffu, none);
+                        const bool odd = m < p.M && zero_times<32>(v) != 0.f;
+                        if (__any_sync(0xffffffffu, odd) || odd_ids) {
+                            for (int j = 0; j < 32 && n + j < p.N; ++j) {
+                                const int id = __shfl_sync(0xffffffffu, id_l, j);
+                                float y = 0.f;
+#pragma unroll
+                                for (int q = 0; q < 32; ++q)
+                                    if (q == j) y = v[q];
+                                if ((odd_ids >> j) & 1u) y = __int_as_float(0x7fc00000);
+                                else if (m < p.M && !isfinite(y))
+                                    y = adapter_element(p.ad, p.ad_S, p.ad_ldS, n + j, m, id, 0, 1);
+                                if (m < p.M) adapter_store(p.ad, n + j, m, y);
+                            }
+                        } else if (m < p.M) {
+                            const float bias = p.ad.bias ? __ldg(p.ad.bias + m) : 0.f;
+                            const size_t ld = (size_t)p.M;
+                            if (p.ad.accumulate) {
+                                float* y = static_cast<float*>(p.ad.y) + (size_t)n * ld + m;
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    if (n + j < p.N) y[j * ld] += v[j] + bias;
+                            } else {
+                                __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.ad.y) + (size_t)n * ld + m;
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) {
+                                    float o = v[j] + bias;
+                                    if (p.ad.act == 1) o = o < 0.f ? 0.f : o;
+                                    if (n + j < p.N) y[j * ld] = __float2bfloat16_rn(o);
+                                }
+                            }
+                        }
+                        continue;
+                    }
                     if (m < p.M) {
                         if (F8) {
                             // E4M3 units back to real ones: times the token's scale (N side),
@@ -778,14 +844,6 @@ __device__ __forceinline__ void dequant_chunk(const TcParams& p, int m, int n, f
         for (int j = 0; j < W; ++j)
             v[j] = v[j] * sa * ((n + j < p.N) ? __ldg(p.b_scale + n + j) : 0.f);
     }
-}
-
-template <int W>
-__device__ __forceinline__ float zero_times(const float* v) {
-    float z[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < W; ++j) z[j & 3] = fmaf(v[j], 0.f, z[j & 3]);
-    return (z[0] + z[1]) + (z[2] + z[3]);
 }
 
 // Pair-kernel epilogue: each warp stages its 32 rows x (32 fp32 | 64 bf16) columns in
@@ -1645,18 +1703,18 @@ int num_sms() {
     return n;
 }
 
-template <int EPI, int BNT, bool F8 = false>
+template <int EPI, int BNT, bool F8 = false, bool LIST = false>
 int launch_epi(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a2,
                const CUtensorMap& b2, const TcParams& p, cudaStream_t st) {
     constexpr int smem = Tile1<BNT>::SMEM_BYTES;
     static std::atomic<uint64_t> attr{0};
-    if (smem_limit(reinterpret_cast<const void*>(gemm_tc_kernel<EPI, BNT, F8>), smem, attr) != cudaSuccess) return 1;
+    if (smem_limit(reinterpret_cast<const void*>(gemm_tc_kernel<EPI, BNT, F8, LIST>), smem, attr) != cudaSuccess) return 1;
     const int items = EPI == EPI_SPLIT_T ? p.n_tiles * p.ksplit : p.n_tiles;
     const int grid = items < num_sms() ? items : num_sms();
     if (EPI == EPI_SPLIT_T)
-        return launch_pdl(gemm_tc_kernel<EPI, BNT, F8>, dim3(grid), dim3(NUM_THREADS), smem, st, a, b,
+        return launch_pdl(gemm_tc_kernel<EPI, BNT, F8, LIST>, dim3(grid), dim3(NUM_THREADS), smem, st, a, b,
                           a2, b2, p) == cudaSuccess ? 0 : 1;
-    gemm_tc_kernel<EPI, BNT, F8><<<grid, NUM_THREADS, smem, st>>>(a, b, a2, b2, p);
+    gemm_tc_kernel<EPI, BNT, F8, LIST><<<grid, NUM_THREADS, smem, st>>>(a, b, a2, b2, p);
     return cudaGetLastError() == cudaSuccess ? 0 : 1;
 }
 
@@ -1876,7 +1934,7 @@ int launch_split_reduce(const GemmArgs& g, const TcParams& p, int ks, cudaStream
         }
     };
     if (g.adapt) {
-        e = launch_adapter_reduce(*g.adapt, g.adapt_S, g.ws, ks, st, pdl);
+        e = launch_adapter_reduce(*g.adapt, *g.adapt_tiles, g.ws, ks, st, pdl);
     } else if (g.epi == EPI_SHRINK) {
         launch_shrink_rows_sum(g.ws, ks, g.M, g.N, g.C, g.ldc, g.c_type, g.row_sign, g.eps,
                                g.scale_cols, g.a_scale, st, pdl);
@@ -1919,7 +1977,11 @@ int gemm_tc_swapped(const GemmArgs& g, cudaStream_t st) {
     CUtensorMap a, b, a2, b2;
     if (!make_map(&a, g.B, g.N, g.K, g.ldb, BM, f8)) return 1;
     if (!make_map(&b, g.A, g.M, g.K, g.lda, bnt, f8)) return 1;
-    if (g.K2 > 0) {
+    if (g.adapt) {
+        const int K2 = g.adapt->n_adapters * g.adapt->rank, ld = g.adapt_tiles->ldS;
+        if (!make_map(&a2, g.adapt->B, g.N, K2, K2, BM)) return 1;
+        if (!make_map(&b2, g.adapt_tiles->S, g.M, ld, ld, bnt)) return 1;
+    } else if (g.K2 > 0) {
         if (!make_map(&a2, g.B2, g.N, g.K2, g.ldb2, BM)) return 1;
         if (!make_map(&b2, g.A2, g.M, g.K2, g.lda2, bnt)) return 1;
     } else {
@@ -1973,6 +2035,19 @@ int gemm_tc_swapped(const GemmArgs& g, cudaStream_t st) {
     ks = effective_splits(p.kb_main, ks, &p.kbs);
     p.ksplit = ks;
     int rc;
+    if (g.adapt) {
+        p.cnt = g.adapt_tiles->cnt; p.list = g.adapt_tiles->list; p.n_list = g.adapt_tiles->n_list;
+        p.ids = g.adapt->ids; p.n_adapters = g.adapt->n_adapters;
+        p.ad = *g.adapt;
+        p.ad_S = static_cast<const __nv_bfloat16*>(g.adapt_tiles->S);
+        p.ad_ldS = g.adapt_tiles->ldS;
+        p.final = ks == 1;
+        rc = bnt == 32   ? launch_epi<EPI_SPLIT_T, 32, false, true>(a, b, a2, b2, p, st)
+             : bnt == 64 ? launch_epi<EPI_SPLIT_T, 64, false, true>(a, b, a2, b2, p, st)
+                         : launch_epi<EPI_SPLIT_T, 128, false, true>(a, b, a2, b2, p, st);
+        if (rc || p.final) return rc;
+        return launch_split_reduce(g, p, ks, st, true);
+    }
     switch (bnt + (f8 ? 1 : 0)) {
         case 32: rc = launch_epi<EPI_SPLIT_T, 32>(a, b, a2, b2, p, st); break;
         case 64: rc = launch_epi<EPI_SPLIT_T, 64>(a, b, a2, b2, p, st); break;
@@ -2118,8 +2193,8 @@ int gemm_tc(const GemmArgs& g, cudaStream_t st) {
         int ks = (2 * pairs + p.n_tiles - 1) / p.n_tiles;
         ks = std::min(ks, std::min(8, p.kb_main / 4));
         while (ks > 1 && (size_t)ks * g.M * g.N > g.ws_floats) --ks;
-        if (ks > 1 || g.adapt) ks = effective_splits(p.kb_main, max(ks, 1), &p.kbs);   // no split without K blocks
-        if (ks > 1 || g.adapt) {
+        if (ks > 1) ks = effective_splits(p.kb_main, ks, &p.kbs);   // no split without K blocks
+        if (ks > 1) {
             p.ksplit = ks;
             CUtensorMap c;
             if (!make_map_ws(&c, g.ws, ks, g.M, g.N)) return 1;

@@ -114,6 +114,11 @@ struct AdapterArgs {
     void* ws; size_t ws_bytes;
 };
 
+// Row blocks (of 256 rows; of 128 in the decode form): the 64-column blocks of the factors that
+// their rows' adapters touch (cnt, list: see TcParams), the masked shrink S [M x ldS] bf16 and the
+// marks of chunks to repair.
+struct AdapterTiles { const int* cnt; const int* list; int n_list; void* S; int ldS; uint8_t* odd; };
+
 struct GemmArgs {
     const void* A; int lda; int a_type;     // [M x K], K contiguous
     const void* B; int ldb; int b_type;     // [N x K], K contiguous
@@ -150,9 +155,10 @@ struct GemmArgs {
     // EPI_STORE / EPI_QKNR with a split reduction: the reduction may also append the k|v
     // columns to the cache (sets *kv_done = 1; else the caller copies them)
     const KvAppend* kv_append; int* kv_done;
-    // a split reduction that also adds each row's own adapter (see AdapterArgs; then launched
-    // behind the kernel that writes adapt_S): bias, activation and output are the adapters'
-    const AdapterArgs* adapt; const float* adapt_S;
+    // decode steps under adapters (M <= 128, a workspace given): the extension blocks are the listed
+    // ones of adapt_tiles; launched behind the kernel that writes its lists and S; bias, activation
+    // and output are the adapters'
+    const AdapterArgs* adapt; const AdapterTiles* adapt_tiles;
 };
 // Split-K residual reduction with the next norm fused (see NormNext); false when the shape or
 // alignment is outside the vectorised form (nothing launched).
@@ -229,13 +235,10 @@ size_t adapter_workspace(int M, int N, int K, int n_adapters, int rank, int dtyp
 cudaError_t launch_linear_adapters_simt(const AdapterArgs& a, cudaStream_t st);
 bool linear_adapters_tc_supported(const AdapterArgs& a);
 cudaError_t launch_linear_adapters_tc(const AdapterArgs& a, cudaStream_t st);
-// y rows from ks fp32 slices ws[ks][M][N], their own adapter's S[m] B_a^T (S fp32 [M x rank]),
-// bias and activation; pdl: a programmatic dependent of the kernel that wrote the slices
-cudaError_t launch_adapter_reduce(const AdapterArgs& a, const float* S, const float* ws, int ks,
+// y rows from ks fp32 slices ws[ks][M][N], bias and activation; pdl: a programmatic dependent of the
+// kernel that wrote the slices
+cudaError_t launch_adapter_reduce(const AdapterArgs& a, const AdapterTiles& t, const float* ws, int ks,
                                   cudaStream_t st, bool pdl);
-// Row blocks of 256: the 64-column blocks of the factors that their rows' adapters touch (cnt,
-// list: see TcParams), the masked shrink S [M x ldS] bf16 and the marks of chunks to repair.
-struct AdapterTiles { const int* cnt; const int* list; int n_list; void* S; int ldS; uint8_t* odd; };
 int gemm_tc_adapters(const AdapterArgs& a, const AdapterTiles& t, cudaStream_t st);   // 0 ok
 
 // ---- objective, estimator, update ------------------------------------------------------
