@@ -113,16 +113,20 @@ __global__ void __launch_bounds__(256) adapter_gemm_kernel(AdapterArgs a, const 
 
 // The rows' shrink for the decode form: S[m, j] = scale[a] x[m] . A_a[j] in fp32, rounded to bf16
 // into row m of the masked S (the products' extension operand), whose other columns become zeros in
-// the blocks that any row uses.  A warp takes JW of the adapter's rows, so that x[m] is read once for
-// them; 16-byte loads; the warps of a CTA share row m through L1.  The first CTA also writes the list
+// the blocks that any row uses.  KW warps share a dot, each with its part of K (few rows: the chain of
+// loads is what takes time), or a warp takes JW of the adapter's rows, so that x[m] is read once for
+// them (many); 16-byte loads; the warps of a CTA share row m through L1.  The first CTA also writes the list
 // of blocks: those that the rows' adapters touch, with the mask of their 16-column steps.
-template <int JW>
+template <int JW, int KW>
 __global__ void __launch_bounds__(SH_WARPS * 32)
     adapter_shrink_rows_kernel(AdapterArgs a, __nv_bfloat16* __restrict__ S, int ldS, int* __restrict__ cnt,
                                int* __restrict__ list) {
     __shared__ unsigned steps[4096 / 32];      // one bit per 16-column step of 65536 columns
     grid_dep_launch();                         // the product reads S and the list only at its end
-    const int groups = (a.rank + JW * SH_WARPS - 1) / (JW * SH_WARPS);
+    constexpr int PER_CTA = JW * SH_WARPS / KW;          // rows of the adapter per CTA
+    static_assert(KW == 1 || (KW == SH_WARPS && JW == 1), "a whole CTA per dot, or a warp");
+    __shared__ float parts[SH_WARPS];
+    const int groups = (a.rank + PER_CTA - 1) / PER_CTA;
     const int m = (int)blockIdx.x / groups, grp = (int)blockIdx.x % groups;
     const int lane = threadIdx.x & 31, n_list = ldS / 64;
     const int id = a.ids[m];
@@ -163,8 +167,9 @@ __global__ void __launch_bounds__(SH_WARPS * 32)
             if (lane == 0) *cnt = used;
         }
     }
-    const int j0 = (grp * SH_WARPS + (int)(threadIdx.x >> 5)) * JW;
-    if (!live || j0 >= a.rank) return;
+    const int warp = (int)(threadIdx.x >> 5), kpart = warp % KW;
+    const int j0 = grp * PER_CTA + warp / KW * JW;
+    if (!live || j0 >= a.rank) return;         // (with KW > 1 the whole CTA)
     const uint4* x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + (size_t)m * a.K);
     const uint4* f[JW];
 #pragma unroll
@@ -175,7 +180,7 @@ __global__ void __launch_bounds__(SH_WARPS * 32)
 #pragma unroll
     for (int q = 0; q < JW; ++q) s[q][0] = s[q][1] = 0.f;
 #pragma unroll 4
-    for (int k = lane; k < a.K / 8; k += 32) {
+    for (int k = kpart * 32 + lane; k < a.K / 8; k += 32 * KW) {
         float xv[8];
         bf8(__ldg(x + k), xv);
 #pragma unroll
@@ -188,20 +193,26 @@ __global__ void __launch_bounds__(SH_WARPS * 32)
     }
 #pragma unroll
     for (int q = 0; q < JW; ++q) {
-        const float v = warp_sum(s[q][0] + s[q][1]);
-        if (lane == 0 && j0 + q < a.rank)
+        float v = warp_sum(s[q][0] + s[q][1]);
+        if (KW > 1) {
+            if (lane == 0) parts[warp] = v;
+            __syncthreads();
+            v = 0.f;
+            for (int w = 0; w < KW; ++w) v += parts[w];
+        }
+        if (lane == 0 && kpart == 0 && j0 + q < a.rank)
             S[(size_t)m * ldS + (size_t)id * a.rank + j0 + q] = __float2bfloat16_rn(v * a.scale[id]);
     }
 }
 
-template <int JW>
+template <int JW, int KW>
 cudaError_t launch_shrink_rows(const AdapterArgs& a, __nv_bfloat16* S, int ldS, int* cnt, int* list,
                                cudaStream_t st) {
     static std::atomic<uint64_t> share{0};
-    const cudaError_t e = smem_share(reinterpret_cast<const void*>(adapter_shrink_rows_kernel<JW>), share);
+    const cudaError_t e = smem_share(reinterpret_cast<const void*>(adapter_shrink_rows_kernel<JW, KW>), share);
     if (e != cudaSuccess) return e;
-    adapter_shrink_rows_kernel<JW>
-        <<<a.M * cdiv(a.rank, JW * SH_WARPS), SH_WARPS * 32, 0, st>>>(a, S, ldS, cnt, list);
+    adapter_shrink_rows_kernel<JW, KW>
+        <<<a.M * cdiv(a.rank, JW * SH_WARPS / KW), SH_WARPS * 32, 0, st>>>(a, S, ldS, cnt, list);
     return cudaGetLastError();
 }
 
@@ -413,9 +424,11 @@ cudaError_t launch_linear_adapters_tc(const AdapterArgs& a, cudaStream_t st) {
         g.adapt_tiles = &at;
         if (!gemm_tc_supported(g)) return cudaErrorNotSupported;
         __nv_bfloat16* S = static_cast<__nv_bfloat16*>(at.S);
-        // four of the adapter's rows per warp once that still fills the SMs
-        const cudaError_t e = a.M * a.rank >= 4 * 148 * SH_WARPS ? launch_shrink_rows<4>(a, S, t.ld, cnt, list, st)
-                                                                 : launch_shrink_rows<1>(a, S, t.ld, cnt, list, st);
+        // dots: under one CTA per SM a CTA each; once warps fill the SMs, four per warp
+        const int dots = a.M * a.rank;
+        const cudaError_t e = dots <= 148                  ? launch_shrink_rows<1, SH_WARPS>(a, S, t.ld, cnt, list, st)
+                              : dots >= 4 * 148 * SH_WARPS ? launch_shrink_rows<4, 1>(a, S, t.ld, cnt, list, st)
+                                                           : launch_shrink_rows<1, 1>(a, S, t.ld, cnt, list, st);
         if (e != cudaSuccess) return e;
         return gemm_tc(g, st) ? cudaErrorUnknown : cudaSuccess;
     }
