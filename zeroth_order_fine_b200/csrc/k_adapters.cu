@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(128)
 __global__ void __launch_bounds__(256)
     adapter_lists_kernel(const int* __restrict__ ids, int M, int n_adapters, int rank, int* __restrict__ cnt,
                          int* __restrict__ list, int n_list) {
+    // (blocks past the last one have no steps)
     __shared__ unsigned steps[4096 / 32];       // one bit per 16-column step of 65536 columns
     __shared__ int wsum[8];
     grid_dep_launch();
@@ -352,8 +353,9 @@ TileSpace tile_space(int M, int N, int K2) {
     TileSpace t;
     const int rows = pass_rows(M, K2);
     t.blocks = (rows + 255) / 256;
-    t.n_list = (K2 + 63) / 64;
-    t.ld = t.n_list * 64;
+    const int blocks = (K2 + 63) / 64;
+    t.n_list = (blocks + 7) / 8 * 8;      // lists are read 8 entries at a time
+    t.ld = blocks * 64;
     t.list = up256((size_t)t.blocks * 4);
     t.s = t.list + up256((size_t)t.blocks * t.n_list * 4);
     t.odd = t.s + up256((size_t)rows * t.ld * 2);
