@@ -26,6 +26,7 @@ constexpr int SH_WARPS = 8;
 // S[m, j] for the rank rows of row m's own adapter: one warp per (m, j), the dot summed over the
 // lanes in a fixed tree.  Rows without an adapter are not written (nor read later).
 __global__ void __launch_bounds__(SH_WARPS * 32) adapter_shrink_kernel(AdapterArgs a, float* S) {
+    grid_dep_launch();                         // the fp32 product does not read S
     const int m = blockIdx.x, lane = threadIdx.x & 31;
     const int j = blockIdx.y * SH_WARPS + (threadIdx.x >> 5);
     const int id = a.ids[m];
@@ -108,6 +109,160 @@ __global__ void __launch_bounds__(256) adapter_gemm_kernel(AdapterArgs a, const 
     }
 }
 
+
+// ---- fp32 -----------------------------------------------------------------------------------
+// The product in fp32 on CUDA cores, bound by their FMA rate (2 M N K flops at ~70 TFLOP/s): 64 x 64
+// tiles, 8 x 4 outputs a thread, K in 32-deep stages by asynchronous 16-byte copies.  The tiles stay
+// as they lie in memory (K contiguous, rows padded to 36 floats): a thread reads 4 of K at a time of
+// its 8 rows and 4 columns, 12 16-byte reads for 128 FMAs, without bank clashes, two FMAs to an
+// instruction (neighbouring k).  K is also split
+// over CTAs where the tiles alone would leave the last round of SMs half empty; each split writes a
+// slice, and the slices are added in order by the kernel that adds the expand.
+constexpr int FM = 64, FK = 32, FLD = FK + 4, FSTAGES = 3, F_THREADS = 128;
+constexpr int F_SMEM = FSTAGES * 2 * FM * FLD * 4;
+
+__device__ __forceinline__ void cp16(uint32_t dst, const float* src, bool live) {
+    const int n = live ? 16 : 0;               // 0: zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+__global__ void __launch_bounds__(F_THREADS)
+    gemm_f32_kernel(const float* __restrict__ A, const float* __restrict__ B, int M, int N, int K, int ks,
+                    float* __restrict__ slices) {
+    extern __shared__ __align__(16) float fsm[];
+    grid_dep_launch();
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int m0 = blockIdx.y * FM, n0 = blockIdx.x * FM, split = blockIdx.z;
+    const int blocks = (K + FK - 1) / FK, per = (blocks + ks - 1) / ks;
+    const int b0 = split * per, b1 = min(blocks, b0 + per);
+    const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(fsm));
+    auto load = [&](int b) {
+        const uint32_t st = base + (uint32_t)((b - b0) % FSTAGES) * (2 * FM * FLD * 4);
+#pragma unroll
+        for (int i = tid; i < 2 * FM * FK / 4; i += F_THREADS) {
+            const int op = i / (FM * FK / 4), r = i / (FK / 4) % FM, c = i % (FK / 4) * 4, k = b * FK + c;
+            const int row = (op ? n0 : m0) + r, rows = op ? N : M;
+            const bool live = row < rows && k < K;
+            const float* src = (op ? B : A) + (live ? (size_t)row * K + k : 0);
+            cp16(st + (uint32_t)((op * FM + r) * FLD + c) * 4, src, live);
+        }
+    };
+    uint64_t acc[8][4];                        // sums over the even and over the odd k
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0ull;
+#pragma unroll
+    for (int s = 0; s < FSTAGES - 1; ++s) {
+        if (b0 + s < b1) load(b0 + s);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    for (int b = b0; b < b1; ++b) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(FSTAGES - 2) : "memory");
+        __syncthreads();                       // stage b is there, and b - 1 has been read
+        if (b + FSTAGES - 1 < b1) load(b + FSTAGES - 1);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        const float* as = fsm + (size_t)((b - b0) % FSTAGES) * (2 * FM * FLD) + ty * FLD;
+        const float* bs = fsm + (size_t)((b - b0) % FSTAGES) * (2 * FM * FLD) + (FM + tx) * FLD;
+#pragma unroll
+        for (int k = 0; k < FK; k += 4) {
+            ulonglong2 x[8], w[4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const ulonglong2*>(as + i * 8 * FLD + k);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const ulonglong2*>(bs + j * 16 * FLD + k);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[i][j]) : "l"(x[i].x), "l"(w[j].x));
+                    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[i][j]) : "l"(x[i].y), "l"(w[j].y));
+                }
+        }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    float* out = slices + (size_t)split * M * N;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int m = m0 + ty + 8 * i;
+        if (m >= M) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int n = n0 + tx + 16 * j;
+            const float2 v = *reinterpret_cast<const float2*>(&acc[i][j]);
+            if (n < N) out[(size_t)m * N + n] = v.x + v.y;
+        }
+    }
+    grid_dep_wait();                           // the shrink before: what follows reads both
+}
+
+// y = act(slices + S[m] B_a^T + b): a CTA takes 4 rows and 128 columns, a thread a column.  Rows of
+// one request lie together, so the factors of a column are read once for a run of rows with the same
+// adapter.
+constexpr int ER = 4;
+__global__ void __launch_bounds__(128)
+    adapter_expand_f32_kernel(AdapterArgs a, const float* __restrict__ S, const float* __restrict__ slices, int ks) {
+    __shared__ __align__(16) float s[ER][256];
+    const int m0 = blockIdx.x * ER, n = blockIdx.y * 128 + threadIdx.x, rows = min(ER, a.M - m0);
+    int id[ER];
+#pragma unroll
+    for (int i = 0; i < ER; ++i) id[i] = i < rows ? a.ids[m0 + i] : -1;
+    grid_dep_wait();
+    for (int i = threadIdx.x; i < rows * a.rank; i += 128) s[i / a.rank][i % a.rank] = S[(size_t)m0 * a.rank + i];
+    __syncthreads();
+    if (n >= a.N) return;
+    float y[ER];
+#pragma unroll
+    for (int i = 0; i < ER; ++i) {
+        y[i] = 0.f;
+        if (i < rows)
+#pragma unroll 4
+            for (int k = 0; k < ks; ++k) y[i] += slices[((size_t)k * a.M + m0 + i) * a.N + n];
+    }
+    const float* B = static_cast<const float*>(a.B) + (size_t)n * a.n_adapters * a.rank;
+#pragma unroll
+    for (int i = 0; i < ER; ++i) {
+        // the run that begins at row i
+        if (i >= rows || id[i] < 0 || id[i] >= a.n_adapters || (i > 0 && id[i] == id[i > 0 ? i - 1 : 0])) continue;
+        int end = i + 1;
+        while (end < rows && a.ids[m0 + end] == id[i]) ++end;
+        const float* b = B + (size_t)id[i] * a.rank;
+        for (int c = 0; c < a.rank; ++c) {
+            const float v = __ldg(b + c);
+#pragma unroll
+            for (int q = i; q < ER; ++q)
+                if (q < end) y[q] = fmaf(s[q][c], v, y[q]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < ER; ++i) {
+        if (i >= rows) continue;
+        float v = y[i];
+        if (id[i] < -1 || id[i] >= a.n_adapters) v = __int_as_float(0x7fc00000);
+        if (a.bias) v += a.bias[n];
+        if (a.act == 1) v = v < 0.f ? 0.f : v;
+        float* o = static_cast<float*>(a.y) + (size_t)(m0 + i) * a.N + n;
+        *o = a.accumulate ? *o + v : v;
+    }
+}
+
+// K splits of the fp32 product: the fewest whose last round of SMs is full enough (each costs a slice)
+int f32_splits(int M, int N, int K) {
+    const long long tiles = (long long)((M + FM - 1) / FM) * ((N + FM - 1) / FM);
+    const int blocks = (K + FK - 1) / FK;
+    int best = 1;
+    double least = 1e300;
+    for (int k = 1; k <= 8 && k <= (blocks + 3) / 4; ++k) {
+        const int per = (blocks + k - 1) / k;
+        if ((blocks + per - 1) / per != k) continue;
+        const double cost = (double)((tiles * k + 147) / 148) * per / blocks + 0.02 * k;
+        if (cost < least) {
+            least = cost;
+            best = k;
+        }
+    }
+    return best;
+}
 
 // ---- tensor-core forms ----------------------------------------------------------------------
 
@@ -366,9 +521,9 @@ TileSpace tile_space(int M, int N, int K2) {
 }  // namespace
 
 size_t adapter_workspace(int M, int N, int K, int n_adapters, int rank, int dtype) {
-    (void)K;
     const size_t s = up256((size_t)M * rank * 4) + 256;
-    if (dtype != E_BF16 || M == 0) return s;
+    if (M == 0) return s;
+    if (dtype != E_BF16) return s + up256((size_t)f32_splits(M, N, K) * M * N * 4);
     size_t t = tile_space(M, N, n_adapters * rank).total;
     if (M <= STEP_ROWS) t += up256(slice_floats(M, N) * 4);
     return t > s ? t : s;
@@ -376,7 +531,25 @@ size_t adapter_workspace(int M, int N, int K, int n_adapters, int rank, int dtyp
 
 cudaError_t launch_linear_adapters_simt(const AdapterArgs& a, cudaStream_t st) {
     float* S = static_cast<float*>(a.ws);
+    static std::atomic<uint64_t> share{0};
+    cudaError_t e = smem_share(reinterpret_cast<const void*>(adapter_shrink_kernel), share);
+    if (e != cudaSuccess) return e;
     adapter_shrink_kernel<<<dim3(a.M, cdiv(a.rank, SH_WARPS)), SH_WARPS * 32, 0, st>>>(a, S);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const uintptr_t mix = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.W);
+    if (a.dtype == E_F32 && a.K % 4 == 0 && mix % 16 == 0) {
+        static std::atomic<uint64_t> attr{0};
+        e = smem_limit(reinterpret_cast<const void*>(gemm_f32_kernel), F_SMEM, attr);
+        if (e != cudaSuccess) return e;
+        float* slices = reinterpret_cast<float*>(static_cast<char*>(a.ws) + up256((size_t)a.M * a.rank * 4));
+        const int ks = f32_splits(a.M, a.N, a.K);
+        e = launch_pdl(gemm_f32_kernel, dim3(cdiv(a.N, FM), cdiv(a.M, FM), ks), dim3(F_THREADS), F_SMEM, st,
+                       static_cast<const float*>(a.x), static_cast<const float*>(a.W), a.M, a.N, a.K, ks, slices);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(adapter_expand_f32_kernel, dim3(cdiv(a.M, ER), cdiv(a.N, 128)), dim3(128), 0, st, a,
+                          static_cast<const float*>(S), static_cast<const float*>(slices), ks);
+    }
     adapter_gemm_kernel<<<dim3(cdiv(a.N, BN), cdiv(a.M, BM)), 256, 0, st>>>(a, S);
     return cudaGetLastError();
 }

@@ -186,21 +186,36 @@ __device__ __forceinline__ void find_tile(const PagedArgs& a, int i, int rows, T
     __syncthreads();
 }
 
-template <int HD>
+// chunks of keys and values in shared memory: two where they fit and come by themselves
+template <int HD, bool FAST>
+constexpr int paged_stages() { return FAST && HD <= 128 ? 2 : 1; }
+
+// Bytes `bytes` of 16 (the rest zeros) to shared memory, asynchronously.
+__device__ __forceinline__ void copy16(void* dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(bytes)
+                 : "memory");
+}
+
+// FAST: fp32 with 16-byte rows: keys and values come by asynchronous 16-byte copies, the next
+// chunk's beside the work on this one; otherwise element by element.
+template <int HD, bool FAST>
 __global__ void __launch_bounds__(A_THREADS) paged_attention_kernel(PagedArgs a) {
     extern __shared__ __align__(16) float sm[];
     constexpr int LD = HD + 4;             // padded rows: 16-byte reads without bank clashes
+    constexpr int STAGES = paged_stages<HD, FAST>();
+    constexpr int PLD = AK + 4;
     float* Qs = sm;                        // [AQ][LD]
-    float* Ks = Qs + AQ * LD;              // [AK][LD]
-    float* Vs = Ks + AK * LD;              // [AK][LD]
-    float* Ps = Vs + AK * LD;              // [AQ][AK + 4]
+    float* Ps = Qs + AQ * LD;              // [AQ][PLD]
+    float* KVs = Ps + AQ * PLD;            // [STAGES][2][AK][LD]
     __shared__ TileAt at;
     __shared__ int wsum[A_THREADS / 32];
     __shared__ int bad_s;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    find_tile(a, blockIdx.x, AQ, &at, wsum);
-    if (at.req < 0) return;
     if (tid == 0) bad_s = 0;
+    find_tile(a, blockIdx.x, AQ, &at, wsum);   // (synchronises the block)
+    if (at.req < 0) return;
     const int r = at.req, kvh = blockIdx.y;
     const int start = a.cu_new[r], n = a.cu_new[r + 1] - start, len = a.lens[r];
     const int row0 = at.tile * AQ;
@@ -212,7 +227,40 @@ __global__ void __launch_bounds__(A_THREADS) paged_attention_kernel(PagedArgs a)
     // the last key any row of the tile sees, plus one
     const int kend = bad_len ? 0 : ctx + (row0 + rows - 1) / a.g + 1;
     const size_t ldc = (size_t)2 * a.Hkv * HD;
+    const int chunks = (kend + AK - 1) / AK;
 
+    // a chunk's keys and values: 4 threads to a row
+    constexpr int PER = HD / 4;            // elements of a thread
+    const int jr = tid >> 2, part = (tid & 3) * PER;
+    auto load = [&](int c) {
+        float* kd = KVs + (size_t)(c % STAGES) * 2 * AK * LD + jr * LD + part;
+        float* vd = kd + AK * LD;
+        const int pos = c * AK + jr;
+        size_t b = 0;
+        bool live = false;
+        if (pos < kend) {
+            const int page = table[pos >> a.page_shift];
+            live = (unsigned)page < (unsigned)n_pages;
+            if (!live) bad_s = 1;
+            else
+                b = (((size_t)page << a.page_shift) + (pos & ((1 << a.page_shift) - 1))) * ldc +
+                    (size_t)kvh * HD + part;
+        }
+        if (FAST) {
+            const float* src = static_cast<const float*>(a.cache) + b;
+#pragma unroll
+            for (int d = 0; d < PER; d += 4) {
+                copy16(kd + d, src + d, live ? 16 : 0);
+                copy16(vd + d, src + (live ? (size_t)a.Hkv * HD : 0) + d, live ? 16 : 0);
+            }
+        } else {
+            for (int d = 0; d < PER; ++d) {
+                kd[d] = live ? ld_elem(a.cache, b + d, a.dtype) : 0.f;
+                vd[d] = live ? ld_elem(a.cache, b + (size_t)a.Hkv * HD + d, a.dtype) : 0.f;
+            }
+        }
+    };
+    if (STAGES > 1 && chunks > 0) load(0);
     for (int i = tid; i < AQ * HD; i += A_THREADS) {
         const int q = i / HD, d = i % HD;
         float v = 0.f;
@@ -222,47 +270,44 @@ __global__ void __launch_bounds__(A_THREADS) paged_attention_kernel(PagedArgs a)
         }
         Qs[q * LD + d] = v;
     }
-    constexpr int DPT = HD / 16;           // output dims of a thread
-    float m[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f}, o[2][DPT];
+    // output dims of a thread: V at tx * VW + 16 VW * i
+    constexpr int VW = HD >= 64 ? 4 : 2, NV = HD / (16 * VW);
+    float m[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f}, o[2][NV][VW];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int d = 0; d < DPT; ++d) o[i][d] = 0.f;
+        for (int d = 0; d < NV; ++d)
+#pragma unroll
+            for (int e = 0; e < VW; ++e) o[i][d][e] = 0.f;
     int lim[2];                            // keys below lim are seen by the thread's rows
 #pragma unroll
-    for (int i = 0; i < 2; ++i) lim[i] = ctx + (row0 + 2 * ty + i) / a.g + 1;
+    for (int i = 0; i < 2; ++i) lim[i] = min(kend, ctx + (row0 + 2 * ty + i) / a.g + 1);
+    // a warp's rows past the tile's take no part in the products
+    const bool warp_live = 4 * (tid >> 5) < rows;
 
-    for (int c0 = 0; c0 < kend; c0 += AK) {
-        __syncthreads();
-        for (int i = tid; i < AK * HD; i += A_THREADS) {
-            const int j = i / HD, d = i % HD, pos = c0 + j;
-            float kx = 0.f, vx = 0.f;
-            if (pos < kend) {
-                const int page = table[pos >> a.page_shift];
-                if ((unsigned)page < (unsigned)n_pages) {
-                    const size_t b = (((size_t)page << a.page_shift) + (pos & ((1 << a.page_shift) - 1))) *
-                                         ldc + (size_t)kvh * HD + d;
-                    kx = ld_elem(a.cache, b, a.dtype);
-                    vx = ld_elem(a.cache, b + (size_t)a.Hkv * HD, a.dtype);
-                } else {
-                    bad_s = 1;
-                }
-            }
-            Ks[j * LD + d] = kx;
-            Vs[j * LD + d] = vx;
+    for (int c = 0; c < chunks; ++c) {
+        if (STAGES == 1) {
+            __syncthreads();
+            load(c);
         }
-        __syncthreads();
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();                   // chunk c is there; chunk c - 1 has been read
+        if (STAGES > 1 && c + 1 < chunks) load(c + 1);
+        const float* Ks = KVs + (size_t)(c % STAGES) * 2 * AK * LD;
+        const float* Vs = Ks + AK * LD;
+        if (!warp_live) continue;
         float s[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
         for (int d = 0; d < HD; d += 4) {
             float4 qv[2], kv[4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) qv[i] = *reinterpret_cast<float4*>(Qs + (2 * ty + i) * LD + d);
+            for (int i = 0; i < 2; ++i) qv[i] = *reinterpret_cast<const float4*>(Qs + (2 * ty + i) * LD + d);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<float4*>(Ks + (tx + 16 * j) * LD + d);
+            for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * LD + d);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -279,7 +324,7 @@ __global__ void __launch_bounds__(A_THREADS) paged_attention_kernel(PagedArgs a)
             float mx = -FLT_MAX;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                see[j] = c0 + tx + 16 * j < min(lim[i], kend);
+                see[j] = c * AK + tx + 16 * j < lim[i];
                 if (see[j]) mx = fmaxf(mx, s[i][j]);
             }
 #pragma unroll
@@ -291,25 +336,46 @@ __global__ void __launch_bounds__(A_THREADS) paged_attention_kernel(PagedArgs a)
             for (int j = 0; j < 4; ++j) {
                 const float p = see[j] ? expf(s[i][j] - mn) : 0.f;
                 sum += p;
-                Ps[(2 * ty + i) * (AK + 4) + tx + 16 * j] = p;
+                Ps[(2 * ty + i) * PLD + tx + 16 * j] = p;
             }
 #pragma unroll
             for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
             l[i] = l[i] * corr + sum;
             m[i] = mn;
 #pragma unroll
-            for (int d = 0; d < DPT; ++d) o[i][d] *= corr;
+            for (int d = 0; d < NV; ++d)
+#pragma unroll
+                for (int e = 0; e < VW; ++e) o[i][d][e] *= corr;
         }
         __syncwarp();                      // a row's P is written and read by one half-warp
-        for (int j = 0; j < AK; ++j) {
-            const float p0 = Ps[(2 * ty) * (AK + 4) + j], p1 = Ps[(2 * ty + 1) * (AK + 4) + j];
+        const int keys = min(AK, kend - c * AK);
+#pragma unroll 2
+        for (int j0 = 0; j0 < keys; j0 += 4) {       // (P and V behind the last key are zeros)
+            float4 pv[2];
 #pragma unroll
-            for (int d = 0; d < DPT; ++d) {
-                const float v = Vs[j * LD + tx + 16 * d];
-                o[0][d] = fmaf(p0, v, o[0][d]);
-                o[1][d] = fmaf(p1, v, o[1][d]);
-            }
+            for (int i = 0; i < 2; ++i) pv[i] = *reinterpret_cast<const float4*>(Ps + (2 * ty + i) * PLD + j0);
+            const float pe[2][4] = {{pv[0].x, pv[0].y, pv[0].z, pv[0].w}, {pv[1].x, pv[1].y, pv[1].z, pv[1].w}};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int d = 0; d < NV; ++d) {
+                    float v[VW];
+                    const float* src = Vs + (j0 + j) * LD + tx * VW + 16 * VW * d;
+                    if constexpr (VW == 4) {
+                        const float4 t = *reinterpret_cast<const float4*>(src);
+                        v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+                    } else {
+                        const float2 t = *reinterpret_cast<const float2*>(src);
+                        v[0] = t.x; v[1] = t.y;
+                    }
+#pragma unroll
+                    for (int e = 0; e < VW; ++e) {
+                        o[0][d][e] = fmaf(pe[0][j], v[e], o[0][d][e]);
+                        o[1][d][e] = fmaf(pe[1][j], v[e], o[1][d][e]);
+                    }
+                }
         }
+        __syncwarp();
     }
     __syncthreads();
 #pragma unroll
@@ -319,20 +385,23 @@ __global__ void __launch_bounds__(A_THREADS) paged_attention_kernel(PagedArgs a)
         const int t = (row0 + q) / a.g, h = kvh * a.g + (row0 + q) % a.g;
         const float inv = (bad_len || bad_s) ? __int_as_float(0x7fc00000) : 1.f / l[i];
 #pragma unroll
-        for (int d = 0; d < DPT; ++d)
-            st_elem(a.out, (size_t)(start + t) * a.ld_out + (size_t)h * HD + tx + 16 * d, a.dtype,
-                    o[i][d] * inv);
+        for (int d = 0; d < NV; ++d)
+#pragma unroll
+            for (int e = 0; e < VW; ++e)
+                st_elem(a.out, (size_t)(start + t) * a.ld_out + (size_t)h * HD + tx * VW + 16 * VW * d + e,
+                        a.dtype, o[i][d][e] * inv);
     }
 }
 
-template <int HD>
+template <int HD, bool FAST>
 cudaError_t launch_paged_hd(const PagedArgs& a, cudaStream_t st) {
-    const size_t smem = sizeof(float) * ((AQ + 2 * AK) * (HD + 4) + AQ * (AK + 4));
+    const size_t smem = sizeof(float) * (AQ * (HD + 4) + AQ * (AK + 4) +
+                                         (size_t)paged_stages<HD, FAST>() * 2 * AK * (HD + 4));
     static std::atomic<uint64_t> attr{0};
-    cudaError_t e = smem_limit(reinterpret_cast<const void*>(paged_attention_kernel<HD>), (int)smem, attr);
+    cudaError_t e = smem_limit(reinterpret_cast<const void*>(paged_attention_kernel<HD, FAST>), (int)smem, attr);
     if (e != cudaSuccess) return e;
     const long long tiles = ((long long)a.n_tokens * a.g + AQ - 1) / AQ + a.n_rows;
-    paged_attention_kernel<HD><<<dim3((unsigned)tiles, a.Hkv), A_THREADS, smem, st>>>(a);
+    paged_attention_kernel<HD, FAST><<<dim3((unsigned)tiles, a.Hkv), A_THREADS, smem, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -397,11 +466,12 @@ cudaError_t launch_kv_write(const void* kv, long long ld_bytes, const int* slots
 
 cudaError_t launch_paged_attention(const PagedArgs& a, cudaStream_t st) {
     if (a.n_tokens <= 0 || a.n_rows <= 0) return cudaSuccess;
+    const bool fast = a.dtype == E_F32 && reinterpret_cast<uintptr_t>(a.cache) % 16 == 0;
     switch (a.hd) {
-        case 32: return launch_paged_hd<32>(a, st);
-        case 64: return launch_paged_hd<64>(a, st);
-        case 128: return launch_paged_hd<128>(a, st);
-        case 256: return launch_paged_hd<256>(a, st);
+        case 32: return fast ? launch_paged_hd<32, true>(a, st) : launch_paged_hd<32, false>(a, st);
+        case 64: return fast ? launch_paged_hd<64, true>(a, st) : launch_paged_hd<64, false>(a, st);
+        case 128: return fast ? launch_paged_hd<128, true>(a, st) : launch_paged_hd<128, false>(a, st);
+        case 256: return fast ? launch_paged_hd<256, true>(a, st) : launch_paged_hd<256, false>(a, st);
         default: return cudaErrorInvalidValue;
     }
 }
