@@ -134,56 +134,44 @@ __global__ void __launch_bounds__(KW_THREADS)
 }
 
 // ---- attention over the pages, CUDA cores ----------------------------------------------------
-// One CTA per (tile of 32 query rows of one request, kv head).  A request's query rows for a kv
+// A work item is (tile of 64 query rows of one request, kv head).  A request's query rows for a kv
 // head are its new tokens times the g query heads that share the head, token-major: row i is token
 // i / g, head kvh * g + i % g.  Keys stream through shared memory in chunks of 64 with an online
 // softmax in fp32; keys a row may not see get probability 0 and value rows behind the request's
-// end are staged as zeros, so what lies there is never part of a result.
-constexpr int AQ = 32, AK = 64, A_THREADS = 256;
+// end are staged as zeros, so what lies there is never part of a result.  The chunks of all items
+// form one line, cut into equal stretches, one per CTA that fits on the SMs; an item cut by a
+// stretch's end is written as partial (m, l, o) and joined by a second kernel in key order.
+constexpr int AQ = 64, AK = 64, A_THREADS = 256;
+constexpr int RT = 4;                      // query rows of a thread, 16 threads side by side on 64 keys
+constexpr int A_GROUPS = 1024;             // prefix entries, in the chunk buffers before their use
+using Line = PagedLine<false, AQ, AK>;
 
-struct TileAt {
-    int req, tile;                         // request and its tile, or req < 0: past the last
-};
+// Floats of a partial result: o [AQ][hd], m [AQ], l [AQ].
+__host__ __device__ constexpr int part_floats(int hd) { return AQ * (hd + 2); }
+// CTAs on an SM: by the registers, and the chunk buffers of the wide heads
+constexpr int paged_ctas(int hd) { return 148 * (hd <= 64 ? 2 : 1); }
 
-// Request and tile of the i-th tile, when request r has ceil(n_r * g / rows) of them.  All
-// threads of the block take part; the answer is in shared memory (out).
-__device__ __forceinline__ int tile_count(const PagedArgs& a, int r, int rows) {
-    const int s = a.cu_new[r], e = a.cu_new[r + 1];
-    if (s < 0 || e < s || e > a.n_tokens) return 0;
-    return (int)(((long long)(e - s) * a.g + rows - 1) / rows);
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
-
-__device__ __forceinline__ void find_tile(const PagedArgs& a, int i, int rows, TileAt* out,
-                                          int* wsum) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-    if (tid == 0) out->req = -1;
-    int base = 0;
-    for (int r0 = 0; r0 < a.n_rows; r0 += blockDim.x) {
-        __syncthreads();                   // wsum free, out written
-        const int r = r0 + tid;
-        const int c = r < a.n_rows ? tile_count(a, r, rows) : 0;
-        int incl = c;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += u;
-        }
-        if (lane == 31) wsum[warp] = incl;
-        __syncthreads();
-        int total = 0, before = 0;
-        for (int w = 0; w < nw; ++w) {
-            if (w < warp) before += wsum[w];
-            total += wsum[w];
-        }
-        const int excl = base + before + incl - c;
-        if (c > 0 && i >= excl && i < excl + c) {
-            out->req = r;
-            out->tile = i - excl;
-        }
-        base += total;
-        if (i < base) break;               // uniform: every thread has the same base
-    }
-    __syncthreads();
+// two fp32 operations to an instruction, each rounded as by itself
+__device__ __forceinline__ uint64_t pair_of(float v) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ void fma_pair(uint64_t& acc, uint64_t a, uint64_t b) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float half_of(uint64_t v, int i) {
+    return __uint_as_float((unsigned)(i ? v >> 32 : v));
 }
 
 // chunks of keys and values in shared memory: two where they fit and come by themselves
@@ -201,7 +189,8 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, int bytes) {
 // FAST: fp32 with 16-byte rows: keys and values come by asynchronous 16-byte copies, the next
 // chunk's beside the work on this one; otherwise element by element.
 template <int HD, bool FAST>
-__global__ void __launch_bounds__(A_THREADS) paged_attention_kernel(PagedArgs a) {
+__global__ void __launch_bounds__(A_THREADS, HD <= 64 ? 2 : 1)
+    paged_attention_kernel(PagedArgs a, PagedDesc* __restrict__ desc, float* __restrict__ part) {
     extern __shared__ __align__(16) float sm[];
     constexpr int LD = HD + 4;             // padded rows: 16-byte reads without bank clashes
     constexpr int STAGES = paged_stages<HD, FAST>();
@@ -209,187 +198,261 @@ __global__ void __launch_bounds__(A_THREADS) paged_attention_kernel(PagedArgs a)
     float* Qs = sm;                        // [AQ][LD]
     float* Ps = Qs + AQ * LD;              // [AQ][PLD]
     float* KVs = Ps + AQ * PLD;            // [STAGES][2][AK][LD]
-    __shared__ TileAt at;
-    __shared__ int wsum[A_THREADS / 32];
     __shared__ int bad_s;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    if (tid == 0) bad_s = 0;
-    find_tile(a, blockIdx.x, AQ, &at, wsum);   // (synchronises the block)
-    if (at.req < 0) return;
-    const int r = at.req, kvh = blockIdx.y;
-    const int start = a.cu_new[r], n = a.cu_new[r + 1] - start, len = a.lens[r];
-    const int row0 = at.tile * AQ;
-    const int rows = min(AQ, (int)min((long long)n * a.g - row0, (long long)AQ));
-    const bool bad_len = len < n || (long long)len > ((long long)a.max_blocks << a.page_shift);
-    const int* table = a.block_table + (size_t)r * a.max_blocks;
+    grid_dep_launch();
+    long long* cum = reinterpret_cast<long long*>(KVs);
+    const long long L = Line::prefix(a, A_GROUPS, cum, cum + A_GROUPS + 1);
+    const int w = blockIdx.x;
+    const long long stretch = (L + gridDim.x - 1) / gridDim.x;
+    const long long u1 = min(L, stretch * (w + 1));
+    long long u = stretch * w;
+    if (tid == 0) desc[w].pieces = 0;
+    if (u >= u1) return;
+    Line::Cursor k = Line::locate(a, A_GROUPS, cum, u);
+
+    const float sl2 = a.scale * 1.4426950408889634f;      // scores in units of ln 2
     const int n_pages = (int)(a.n_slots >> a.page_shift);
-    const int ctx = len - n;
-    // the last key any row of the tile sees, plus one
-    const int kend = bad_len ? 0 : ctx + (row0 + rows - 1) / a.g + 1;
     const size_t ldc = (size_t)2 * a.Hkv * HD;
-    const int chunks = (kend + AK - 1) / AK;
-
-    // a chunk's keys and values: 4 threads to a row
-    constexpr int PER = HD / 4;            // elements of a thread
-    const int jr = tid >> 2, part = (tid & 3) * PER;
-    auto load = [&](int c) {
-        float* kd = KVs + (size_t)(c % STAGES) * 2 * AK * LD + jr * LD + part;
-        float* vd = kd + AK * LD;
-        const int pos = c * AK + jr;
-        size_t b = 0;
-        bool live = false;
-        if (pos < kend) {
-            const int page = table[pos >> a.page_shift];
-            live = (unsigned)page < (unsigned)n_pages;
-            if (!live) bad_s = 1;
-            else
-                b = (((size_t)page << a.page_shift) + (pos & ((1 << a.page_shift) - 1))) * ldc +
-                    (size_t)kvh * HD + part;
-        }
-        if (FAST) {
-            const float* src = static_cast<const float*>(a.cache) + b;
-#pragma unroll
-            for (int d = 0; d < PER; d += 4) {
-                copy16(kd + d, src + d, live ? 16 : 0);
-                copy16(vd + d, src + (live ? (size_t)a.Hkv * HD : 0) + d, live ? 16 : 0);
-            }
-        } else {
-            for (int d = 0; d < PER; ++d) {
-                kd[d] = live ? ld_elem(a.cache, b + d, a.dtype) : 0.f;
-                vd[d] = live ? ld_elem(a.cache, b + (size_t)a.Hkv * HD + d, a.dtype) : 0.f;
-            }
-        }
-    };
-    if (STAGES > 1 && chunks > 0) load(0);
-    for (int i = tid; i < AQ * HD; i += A_THREADS) {
-        const int q = i / HD, d = i % HD;
-        float v = 0.f;
-        if (q < rows) {
-            const int t = (row0 + q) / a.g, h = kvh * a.g + (row0 + q) % a.g;
-            v = ld_elem(a.q, (size_t)(start + t) * a.ld_q + (size_t)h * HD + d, a.dtype) * a.scale;
-        }
-        Qs[q * LD + d] = v;
-    }
-    // output dims of a thread: V at tx * VW + 16 VW * i
+    constexpr int PER = HD / 4;            // a chunk's keys and values: 4 threads to a row
+    const int jr = tid >> 2, lane_col = (tid & 3) * PER;
+    // output dims of a thread: VW at tx * VW + 16 VW * i
     constexpr int VW = HD >= 64 ? 4 : 2, NV = HD / (16 * VW);
-    float m[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f}, o[2][NV][VW];
+    while (u < u1) {
+        const int row0 = k.tile * AQ, rows = min(AQ, k.q.rows - row0), kvh = k.head;
+        const int first = k.unit, chunks = (int)min((long long)k.units, k.unit + (u1 - u));
+        const int kend = Line::keys(a, k.q, row0 + AQ);
+        const int* table = a.block_table + (size_t)k.r * a.max_blocks;
+        __syncthreads();                   // what the piece before (or the search) read is free
+        if (tid == 0) bad_s = 0;
+        __syncthreads();
+        // the page of the thread's row in the next chunk to load, fetched a chunk ahead
+        auto page_at = [&](int c) { return c * AK + jr < kend ? table[(c * AK + jr) >> a.page_shift] : 0; };
+        int next_page = page_at(first);
+        auto load = [&](int c) {
+            float* kd = KVs + (size_t)(c % STAGES) * 2 * AK * LD + jr * LD + lane_col;
+            float* vd = kd + AK * LD;
+            const int pos = c * AK + jr;
+            const int page = next_page;
+            next_page = page_at(c + 1);
+            size_t b = 0;
+            bool live = false;
+            if (pos < kend) {
+                live = (unsigned)page < (unsigned)n_pages;
+                if (!live) bad_s = 1;
+                else
+                    b = (((size_t)page << a.page_shift) + (pos & ((1 << a.page_shift) - 1))) * ldc +
+                        (size_t)kvh * HD + lane_col;
+            }
+            if (FAST) {
+                const float* src = static_cast<const float*>(a.cache) + b;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int d = 0; d < NV; ++d)
-#pragma unroll
-            for (int e = 0; e < VW; ++e) o[i][d][e] = 0.f;
-    int lim[2];                            // keys below lim are seen by the thread's rows
-#pragma unroll
-    for (int i = 0; i < 2; ++i) lim[i] = min(kend, ctx + (row0 + 2 * ty + i) / a.g + 1);
-    // a warp's rows past the tile's take no part in the products
-    const bool warp_live = 4 * (tid >> 5) < rows;
-
-    for (int c = 0; c < chunks; ++c) {
-        if (STAGES == 1) {
-            __syncthreads();
-            load(c);
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        __syncthreads();                   // chunk c is there; chunk c - 1 has been read
-        if (STAGES > 1 && c + 1 < chunks) load(c + 1);
-        const float* Ks = KVs + (size_t)(c % STAGES) * 2 * AK * LD;
-        const float* Vs = Ks + AK * LD;
-        if (!warp_live) continue;
-        float s[2][4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 4
-        for (int d = 0; d < HD; d += 4) {
-            float4 qv[2], kv[4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) qv[i] = *reinterpret_cast<const float4*>(Qs + (2 * ty + i) * LD + d);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * LD + d);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
-                    s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
-                    s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
-                    s[i][j] = fmaf(qv[i].w, kv[j].w, s[i][j]);
+                for (int d = 0; d < PER; d += 4) {
+                    copy16(kd + d, src + d, live ? 16 : 0);
+                    copy16(vd + d, src + (live ? (size_t)a.Hkv * HD : 0) + d, live ? 16 : 0);
                 }
+            } else {
+                for (int d = 0; d < PER; ++d) {
+                    kd[d] = live ? ld_elem(a.cache, b + d, a.dtype) : 0.f;
+                    vd[d] = live ? ld_elem(a.cache, b + (size_t)a.Hkv * HD + d, a.dtype) : 0.f;
+                }
+            }
+        };
+        if (STAGES > 1) load(first);
+        for (int i = tid; i < AQ * HD; i += A_THREADS) {
+            const int q = i / HD, d = i % HD;
+            float v = 0.f;
+            if (q < rows) {
+                const int t = (row0 + q) / a.g, h = kvh * a.g + (row0 + q) % a.g;
+                v = ld_elem(a.q, (size_t)(k.q.start + t) * a.ld_q + (size_t)h * HD + d, a.dtype) * sl2;
+            }
+            Qs[q * LD + d] = v;
         }
+        float m[RT], l[RT];
+        uint64_t o[RT][NV][VW / 2];        // pairs of neighbouring dims
+        int lim[RT];                       // keys below lim are seen by the thread's rows
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            bool see[4];
-            float mx = -FLT_MAX;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                see[j] = c * AK + tx + 16 * j < lim[i];
-                if (see[j]) mx = fmaxf(mx, s[i][j]);
-            }
-#pragma unroll
-            for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-            const float mn = fmaxf(m[i], mx);
-            const float corr = expf(m[i] - mn);
-            float sum = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float p = see[j] ? expf(s[i][j] - mn) : 0.f;
-                sum += p;
-                Ps[(2 * ty + i) * PLD + tx + 16 * j] = p;
-            }
-#pragma unroll
-            for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-            l[i] = l[i] * corr + sum;
-            m[i] = mn;
+        for (int i = 0; i < RT; ++i) {
+            m[i] = -FLT_MAX;
+            l[i] = 0.f;
+            lim[i] = min(kend, k.q.ctx + (row0 + RT * ty + i) / a.g + 1);
 #pragma unroll
             for (int d = 0; d < NV; ++d)
 #pragma unroll
-                for (int e = 0; e < VW; ++e) o[i][d][e] *= corr;
+                for (int e = 0; e < VW / 2; ++e) o[i][d][e] = 0ull;
         }
-        __syncwarp();                      // a row's P is written and read by one half-warp
-        const int keys = min(AK, kend - c * AK);
+        // a warp's rows past the tile's take no part in the products
+        const bool warp_live = 2 * RT * (tid >> 5) < rows;
+
+        for (int c = first; c < chunks; ++c) {
+            if (STAGES == 1) {
+                __syncthreads();
+                load(c);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncthreads();               // chunk c is there; chunk c - 1 has been read
+            if (STAGES > 1 && c + 1 < chunks) load(c + 1);
+            const float* Ks = KVs + (size_t)(c % STAGES) * 2 * AK * LD;
+            const float* Vs = Ks + AK * LD;
+            if (!warp_live) continue;
+            float s[RT][4];
+            {
+                uint64_t s2[RT][4];        // sums over the even and over the odd dims
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s2[i][j] = 0ull;
+#pragma unroll 4
+                for (int d = 0; d < HD; d += 4) {
+                    ulonglong2 qv[RT], kv[4];
+#pragma unroll
+                    for (int i = 0; i < RT; ++i)
+                        qv[i] = *reinterpret_cast<const ulonglong2*>(Qs + (RT * ty + i) * LD + d);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        kv[j] = *reinterpret_cast<const ulonglong2*>(Ks + (tx + 16 * j) * LD + d);
+#pragma unroll
+                    for (int i = 0; i < RT; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            fma_pair(s2[i][j], qv[i].x, kv[j].x);
+                            fma_pair(s2[i][j], qv[i].y, kv[j].y);
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[i][j] = half_of(s2[i][j], 0) + half_of(s2[i][j], 1);
+            }
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                bool see[4];
+                float mx = -FLT_MAX;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    see[j] = c * AK + tx + 16 * j < lim[i];
+                    if (see[j]) mx = fmaxf(mx, s[i][j]);
+                }
+#pragma unroll
+                for (int x = 8; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+                const float mn = fmaxf(m[i], mx);
+                const float corr = ex2(m[i] - mn);
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float p = see[j] ? ex2(s[i][j] - mn) : 0.f;
+                    sum += p;
+                    Ps[(RT * ty + i) * PLD + tx + 16 * j] = p;
+                }
+#pragma unroll
+                for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                l[i] = l[i] * corr + sum;
+                m[i] = mn;
+                const uint64_t cc = pair_of(corr);
+#pragma unroll
+                for (int d = 0; d < NV; ++d)
+#pragma unroll
+                    for (int e = 0; e < VW / 2; ++e) o[i][d][e] = mul_pair(o[i][d][e], cc);
+            }
+            __syncwarp();                  // a row's P is written and read by one half-warp
+            const int keys = min(AK, kend - c * AK);
 #pragma unroll 2
-        for (int j0 = 0; j0 < keys; j0 += 4) {       // (P and V behind the last key are zeros)
-            float4 pv[2];
+            for (int j0 = 0; j0 < keys; j0 += 4) {       // (P and V behind the last key are zeros)
+                uint64_t pe[RT][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) pv[i] = *reinterpret_cast<const float4*>(Ps + (2 * ty + i) * PLD + j0);
-            const float pe[2][4] = {{pv[0].x, pv[0].y, pv[0].z, pv[0].w}, {pv[1].x, pv[1].y, pv[1].z, pv[1].w}};
+                for (int i = 0; i < RT; ++i) {
+                    const float4 t = *reinterpret_cast<const float4*>(Ps + (RT * ty + i) * PLD + j0);
+                    pe[i][0] = pair_of(t.x); pe[i][1] = pair_of(t.y);
+                    pe[i][2] = pair_of(t.z); pe[i][3] = pair_of(t.w);
+                }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int d = 0; d < NV; ++d) {
-                    float v[VW];
-                    const float* src = Vs + (j0 + j) * LD + tx * VW + 16 * VW * d;
-                    if constexpr (VW == 4) {
-                        const float4 t = *reinterpret_cast<const float4*>(src);
-                        v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
-                    } else {
-                        const float2 t = *reinterpret_cast<const float2*>(src);
-                        v[0] = t.x; v[1] = t.y;
+                    for (int d = 0; d < NV; ++d) {
+                        uint64_t v[VW / 2];
+                        const float* src = Vs + (j0 + j) * LD + tx * VW + 16 * VW * d;
+                        if constexpr (VW == 4) {
+                            const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(src);
+                            v[0] = t.x; v[1] = t.y;
+                        } else {
+                            v[0] = *reinterpret_cast<const uint64_t*>(src);
+                        }
+#pragma unroll
+                        for (int e = 0; e < VW / 2; ++e)
+#pragma unroll
+                            for (int i = 0; i < RT; ++i) fma_pair(o[i][d][e], pe[i][j], v[e]);
                     }
+            }
+            __syncwarp();
+        }
+        __syncthreads();                   // bad_s is final
+        const bool bad = k.q.bad || bad_s;
+        const bool whole = first == 0 && chunks == k.units;
+        float* p = part + (size_t)(2 * w + (first == 0 ? 1 : 0)) * part_floats(HD);
 #pragma unroll
-                    for (int e = 0; e < VW; ++e) {
-                        o[0][d][e] = fmaf(pe[0][j], v[e], o[0][d][e]);
-                        o[1][d][e] = fmaf(pe[1][j], v[e], o[1][d][e]);
-                    }
+        for (int i = 0; i < RT; ++i) {
+            const int q = RT * ty + i;
+            if (q >= rows) continue;
+            if (bad) l[i] = __int_as_float(0x7fc00000);
+            if (!whole && tx == 0) {
+                p[AQ * HD + q] = m[i];
+                p[AQ * HD + AQ + q] = l[i];
+            }
+            const int t = (row0 + q) / a.g, h = kvh * a.g + (row0 + q) % a.g;
+            const size_t out = (size_t)(k.q.start + t) * a.ld_out + (size_t)h * HD;
+            const float inv = 1.f / l[i];
+#pragma unroll
+            for (int d = 0; d < NV; ++d)
+#pragma unroll
+                for (int e = 0; e < VW; ++e) {
+                    const int col = tx * VW + 16 * VW * d + e;
+                    const float v = half_of(o[i][d][e / 2], e & 1);
+                    if (whole) st_elem(a.out, out + col, a.dtype, v * inv);
+                    else p[q * HD + col] = v;
                 }
         }
-        __syncwarp();
+        if (!whole && first == 0 && tid == 0) {
+            PagedDesc d;
+            d.pieces = (int)((u + k.units - 1) / stretch) - w + 1;
+            d.start = k.q.start;
+            d.row0 = row0;
+            d.rows = rows;
+            d.kvh = kvh;
+            desc[w] = d;
+        }
+        u += chunks - first;
+        Line::advance(a, k, chunks - first, u < u1);
     }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int q = 2 * ty + i;
-        if (q >= rows) continue;
-        const int t = (row0 + q) / a.g, h = kvh * a.g + (row0 + q) % a.g;
-        const float inv = (bad_len || bad_s) ? __int_as_float(0x7fc00000) : 1.f / l[i];
-#pragma unroll
-        for (int d = 0; d < NV; ++d)
-#pragma unroll
-            for (int e = 0; e < VW; ++e)
-                st_elem(a.out, (size_t)(start + t) * a.ld_out + (size_t)h * HD + tx * VW + 16 * VW * d + e,
-                        a.dtype, o[i][d][e] * inv);
+}
+
+// Adds the pieces of the item that CTA blockIdx.x's stretch ended inside, in key order: 4 dims of a
+// row per thread and turn.
+template <int HD>
+__global__ void __launch_bounds__(A_THREADS)
+    paged_attention_join_kernel(PagedArgs a, const PagedDesc* __restrict__ desc, const float* __restrict__ part) {
+    grid_dep_wait();
+    const int w = blockIdx.x;
+    const PagedDesc t = desc[w];
+    if (t.pieces <= 0) return;
+    auto piece = [&](int i) { return part + (size_t)(2 * (w + i) + (i == 0 ? 1 : 0)) * part_floats(HD); };
+    constexpr int V = HD / 4;
+    for (int i = threadIdx.x; i < t.rows * V; i += A_THREADS) {
+        const int q = i / V, d = i % V * 4;
+        float m = -FLT_MAX, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int z = 0; z < t.pieces; ++z) m = fmaxf(m, piece(z)[AQ * HD + q]);
+#pragma unroll 4
+        for (int z = 0; z < t.pieces; ++z) {
+            const float* s = piece(z);
+            const float f = ex2(s[AQ * HD + q] - m);
+            const float4 v = *reinterpret_cast<const float4*>(s + q * HD + d);
+            l = fmaf(f, s[AQ * HD + AQ + q], l);
+            o[0] = fmaf(f, v.x, o[0]); o[1] = fmaf(f, v.y, o[1]);
+            o[2] = fmaf(f, v.z, o[2]); o[3] = fmaf(f, v.w, o[3]);
+        }
+        const int tok = (t.row0 + q) / a.g, h = t.kvh * a.g + (t.row0 + q) % a.g;
+        for (int e = 0; e < 4; ++e)
+            st_elem(a.out, (size_t)(t.start + tok) * a.ld_out + (size_t)h * HD + d + e, a.dtype, o[e] / l);
     }
 }
 
@@ -397,12 +460,18 @@ template <int HD, bool FAST>
 cudaError_t launch_paged_hd(const PagedArgs& a, cudaStream_t st) {
     const size_t smem = sizeof(float) * (AQ * (HD + 4) + AQ * (AK + 4) +
                                          (size_t)paged_stages<HD, FAST>() * 2 * AK * (HD + 4));
+    static_assert(2 * AK * (HD + 4) * 4 >= (A_GROUPS + 1 + A_THREADS / 32) * 8, "room for the prefix sums");
     static std::atomic<uint64_t> attr{0};
     cudaError_t e = smem_limit(reinterpret_cast<const void*>(paged_attention_kernel<HD, FAST>), (int)smem, attr);
     if (e != cudaSuccess) return e;
-    const long long tiles = ((long long)a.n_tokens * a.g + AQ - 1) / AQ + a.n_rows;
-    paged_attention_kernel<HD, FAST><<<dim3((unsigned)tiles, a.Hkv), A_THREADS, smem, st>>>(a);
-    return cudaGetLastError();
+    const int grid = paged_ctas(HD);
+    PagedDesc* desc = static_cast<PagedDesc*>(a.ws);
+    float* part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + grid * sizeof(PagedDesc));
+    paged_attention_kernel<HD, FAST><<<grid, A_THREADS, smem, st>>>(a, desc, part);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_pdl(paged_attention_join_kernel<HD>, dim3(grid), dim3(A_THREADS), 0, st, a,
+                      static_cast<const PagedDesc*>(desc), static_cast<const float*>(part));
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -464,8 +533,14 @@ cudaError_t launch_kv_write(const void* kv, long long ld_bytes, const int* slots
     return cudaGetLastError();
 }
 
-cudaError_t launch_paged_attention(const PagedArgs& a, cudaStream_t st) {
+size_t paged_attention_workspace(int hd) {
+    return paged_ctas(hd) * (sizeof(PagedDesc) + (size_t)2 * part_floats(hd) * sizeof(float));
+}
+
+cudaError_t launch_paged_attention(PagedArgs a, cudaStream_t st) {
     if (a.n_tokens <= 0 || a.n_rows <= 0) return cudaSuccess;
+    a.line_heads = a.Hkv;
+    a.step_tokens = 0x7fffffff;            // every request
     const bool fast = a.dtype == E_F32 && reinterpret_cast<uintptr_t>(a.cache) % 16 == 0;
     switch (a.hd) {
         case 32: return fast ? launch_paged_hd<32, true>(a, st) : launch_paged_hd<32, false>(a, st);

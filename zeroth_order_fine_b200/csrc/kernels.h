@@ -221,7 +221,8 @@ struct PagedArgs {
     int step_tokens;                        // requests of at most so many new tokens take the
                                             // decode-step kernel
 };
-cudaError_t launch_paged_attention(const PagedArgs& a, cudaStream_t st);   // CUDA cores
+cudaError_t launch_paged_attention(PagedArgs a, cudaStream_t st);          // CUDA cores
+size_t paged_attention_workspace(int hd);
 bool paged_tc_supported(const PagedArgs& a);                               // bf16, head_dim 64 or 128
 cudaError_t launch_paged_step(PagedArgs a, cudaStream_t st);
 size_t paged_step_workspace(int hd);

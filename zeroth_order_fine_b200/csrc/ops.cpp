@@ -327,9 +327,12 @@ int zo_op_kv_write(const void* qkv, int64_t ld_qkv, const int32_t* slot_map, int
 
 size_t zo_op_attention_paged_workspace(int32_t n_tokens, int32_t n_rows, int32_t n_heads,
                                        int32_t n_kv_heads, int32_t head_dim, int32_t dtype) {
-    (void)n_tokens; (void)n_rows; (void)n_heads; (void)n_kv_heads;
-    if (dtype != ZO_DTYPE_BF16 || (head_dim != 64 && head_dim != 128)) return 256;
-    return std::max(paged_step_workspace(head_dim), paged_chunk_workspace(head_dim));
+    if (n_tokens < 0 || n_rows < 0 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads || head_dim < 1)
+        return 0;
+    size_t n = paged_attention_workspace(head_dim);
+    if (dtype == ZO_DTYPE_BF16 && (head_dim == 64 || head_dim == 128))
+        n = std::max(n, std::max(paged_step_workspace(head_dim), paged_chunk_workspace(head_dim)));
+    return n;
 }
 
 int zo_op_attention_paged(const void* q, int64_t ld_q, const void* cache, int64_t n_slots,
