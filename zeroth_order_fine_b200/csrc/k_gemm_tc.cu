@@ -1097,8 +1097,9 @@ __device__ __forceinline__ int tile_row(int t, const TcParams& p) {
 // instead of 744).
 struct BlockList {
     static constexpr int N = 8;              // entries kept; lists are padded to a multiple of them
-    int cnt, e[N];
-    __device__ __forceinline__ void load(const TcParams& p, int mb) {
+    int mb, cnt, e[N];
+    __device__ __forceinline__ void load(const TcParams& p, int t) {
+        mb = tile_row(t, p);
         cnt = __ldg(p.cnt + mb);
         const int4* l = reinterpret_cast<const int4*>(p.list + (size_t)mb * p.n_list);
 #pragma unroll
@@ -1107,7 +1108,7 @@ struct BlockList {
             e[4 * i] = v.x; e[4 * i + 1] = v.y; e[4 * i + 2] = v.z; e[4 * i + 3] = v.w;
         }
     }
-    __device__ __forceinline__ int get(const TcParams& p, int mb, int i) const {
+    __device__ __forceinline__ int get(const TcParams& p, int i) const {
         if (i >= N) return __ldg(p.list + (size_t)mb * p.n_list + i);
         int v = 0;
 #pragma unroll
@@ -1194,12 +1195,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             uint32_t ph = 0;
             bool ok = true;
             BlockList next;
-            if (LIST && pair < n_items) next.load(p, tile_row(pair, p));
+            if (LIST && pair < n_items) next.load(p, pair);
             for (int t = pair; t < n_items && ok; t += n_pairs) {
                 int mb, nb;
                 tile_coords2(SPLIT ? t / p.ksplit : t, p, &mb, &nb);
                 const BlockList list = next;
-                if (LIST && t + n_pairs < n_items) next.load(p, tile_row(t + n_pairs, p));
                 const int row_a = mb * BM2 + (int)rank * 128;
                 const int row_b = nb * BN + (int)rank * 128;
                 int kb0, n_main, n_kb;
@@ -1228,7 +1228,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                 for (int i = 0; LIST && ok && i < list.cnt; ++i) {
                     if (!mbar_wait(empty(s), ph ^ 1u, abort_f, p.err, p.wait_cycles)) { ok = false; break; }
                     const uint32_t sa = base + s * STAGE2_BYTES;
-                    const int k = (list.get(p, mb, i) & 0xFFFF) * BK;
+                    const int k = (list.get(p, i) & 0xFFFF) * BK;
                     if (rank == 0) mbar_expect_tx(full(s), 2 * STAGE2_BYTES);
                     const uint32_t lb = map_rank(full(s), 0);
                     tma_load_2d_pair(sa, &tmA2, lb, k, row_a);
@@ -1236,6 +1236,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                     ++n_armed;
                     if (++s == STAGES2) { s = 0; ph ^= 1u; }
                 }
+                if (LIST && t + n_pairs < n_items) next.load(p, t + n_pairs);
             }
         }
     } else if (warp == 1) {
@@ -1246,13 +1247,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             uint32_t aph = 0;
             bool ok = true;
             BlockList next;
-            if (LIST && pair < n_items) next.load(p, tile_row(pair, p));
+            if (LIST && pair < n_items) next.load(p, pair);
             for (int t = pair; t < n_items && ok; t += n_pairs) {
                 if (!mbar_wait(tempty(acc), aph ^ 1u, abort_f, p.err, p.wait_cycles)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(acc * BN);
                 const BlockList list = next;
-                if (LIST && t + n_pairs < n_items) next.load(p, tile_row(t + n_pairs, p));
                 int kb0, n_main, n_kb;
                 item_blocks(SPLIT ? t % p.ksplit : 0, &kb0, &n_main, &n_kb);
                 for (int i = 0; i < n_kb; ++i) {
@@ -1277,7 +1277,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                     if (++s == STAGES2) { s = 0; ph ^= 1u; }
                 }
                 for (int i = 0; LIST && ok && i < list.cnt; ++i) {
-                    const int steps = list.get(p, tile_row(t, p), i) >> 16;
+                    const int steps = list.get(p, i) >> 16;
                     if (!mbar_wait(full(s), ph, abort_f, p.err, p.wait_cycles)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t sa = base + s * STAGE2_BYTES;
@@ -1291,6 +1291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                 if (!ok) break;
                 tc_commit_pair(tfull(acc));         // both halves of the accumulator ready
                 if (++acc == 2) { acc = 0; aph ^= 1u; }
+                if (LIST && t + n_pairs < n_items) next.load(p, t + n_pairs);
             }
         }
     } else {

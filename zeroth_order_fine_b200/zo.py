@@ -7,7 +7,6 @@ the import of any entry point raises: there is no fallback path.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Dict, List, Optional, Sequence
@@ -206,11 +205,6 @@ def _stream(stream=None) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _raw_stream(dev: int) -> int:
-    """The current stream of device dev as a cudaStream_t."""
-    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _check(rc: int, handle=None) -> None:
@@ -691,27 +685,38 @@ def zo_op_lm_head_logprob_noalloc(h: torch.Tensor, E: torch.Tensor, targets: tor
 # ---- serving ops: a paged key/value cache and per-request adapters -----------------------
 
 _I32 = (torch.int32,)
-_HERE_ALREADY = contextlib.nullcontext()
 
 
-def _on(name: str, t):
-    """The tensor's device as the current one: a call queues on that device's current stream,
-    whichever device the caller has current."""
+def _queue(dev: int, fn, *args) -> None:
+    """fn(*args, stream) on device dev's current stream, with dev as the current device, whichever
+    device the caller has current."""
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if rc != ZO_OK:
+        _check_op(rc)
+
+
+def _device_of(name: str, t) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    return _HERE_ALREADY if t.get_device() == torch.cuda.current_device() \
-        else torch.cuda.device(t.device)
+    return t.get_device()
 
 
 def _fits(dev: int, *checks) -> bool:
     """Whether every (tensor, dtype, shape) is a contiguous CUDA tensor on device dev like that.
     Decode-step calls are short, so the usual case costs one pass of cheap tests; when it fails,
     _cuda_args finds what is wrong and says so."""
-    for t, dtype, shape in checks:
-        if not (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype
-                and t.shape == shape and t.is_contiguous()):
-            return False
-    return dev >= 0
+    try:
+        for t, dtype, shape in checks:
+            if (t.get_device() != dev or t.dtype is not dtype or t.shape != shape
+                    or not t.is_contiguous()):
+                return False
+    except AttributeError:                 # not a tensor
+        return False
+    return True
 
 
 def _dtype_id(dt: torch.dtype) -> int:
@@ -722,13 +727,17 @@ def _rows(name: str, t, cols: int, dtypes) -> int:
     """Row stride of a 2-d CUDA tensor with at least cols columns, contiguous within a row."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2 or t.shape[1] < cols or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be [rows x >= {cols}], contiguous within a row")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
-    if t.shape[0] > 1 and t.stride(0) < cols:
-        raise ValueError(f"{name} has overlapping rows")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], cols)
+    if t.dim() == 2:
+        (r, c), (row, col) = t.shape, t.stride()
+        if c >= cols and (col == 1 or c == 1):
+            if r <= 1:
+                return c
+            if row >= cols:
+                return row
+            raise ValueError(f"{name} has overlapping rows")
+    raise ValueError(f"{name} must be [rows x >= {cols}], contiguous within a row")
 
 
 def zo_page_ring(n_pages: int, device="cuda"):
@@ -749,30 +758,28 @@ def zo_op_block_tables(old_lens: torch.Tensor, new_lens: torch.Tensor, block_tab
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be [requests x max_blocks]")
     R, max_blocks = block_table.shape
-    with _on("old_lens", old_lens):
-        if cu_new is None:
-            cu_new = torch.empty(R + 1, dtype=torch.int32, device=old_lens.device)
-        if slot_map is None:
-            if max_tokens is None:
-                raise ValueError("give slot_map or max_tokens")
-            slot_map = torch.empty(max_tokens, dtype=torch.int32, device=old_lens.device)
-        dev, i32 = old_lens.get_device(), torch.int32
-        T = slot_map.numel() if max_tokens is None else max_tokens
-        if not _fits(dev, (old_lens, i32, (R,)), (new_lens, i32, (R,)),
-                     (block_table, i32, (R, max_blocks)), (free_ring, i32, free_ring.shape[:1]),
-                     (state, i32, (4,)), (state_out, i32, (4,)), (cu_new, i32, (R + 1,)),
-                     (slot_map, i32, (T,))):
-            _cuda_args({"old_lens": (R,), "new_lens": (R,), "free_ring": (None,), "state": (4,),
-                        "state_out": (4,), "cu_new": (R + 1,), "slot_map": (T,)},
-                       dict.fromkeys(("old_lens", "new_lens", "block_table", "free_ring", "state",
-                                      "state_out", "cu_new", "slot_map"), _I32),
-                       old_lens=old_lens, new_lens=new_lens, block_table=block_table,
-                       free_ring=free_ring, state=state, state_out=state_out, cu_new=cu_new,
-                       slot_map=slot_map)
-        _check_op(lib().zo_op_block_tables(
-            old_lens.data_ptr(), new_lens.data_ptr(), R, page_size, block_table.data_ptr(),
-            max_blocks, free_ring.data_ptr(), free_ring.shape[0], state.data_ptr(),
-            state_out.data_ptr(), cu_new.data_ptr(), slot_map.data_ptr(), T, _raw_stream(dev)))
+    dev, i32 = _device_of("old_lens", old_lens), torch.int32
+    if cu_new is None:
+        cu_new = torch.empty(R + 1, dtype=i32, device=old_lens.device)
+    if slot_map is None:
+        if max_tokens is None:
+            raise ValueError("give slot_map or max_tokens")
+        slot_map = torch.empty(max_tokens, dtype=i32, device=old_lens.device)
+    T = slot_map.numel() if max_tokens is None else max_tokens
+    if not _fits(dev, (old_lens, i32, (R,)), (new_lens, i32, (R,)),
+                 (block_table, i32, (R, max_blocks)), (free_ring, i32, free_ring.shape[:1]),
+                 (state, i32, (4,)), (state_out, i32, (4,)), (cu_new, i32, (R + 1,)),
+                 (slot_map, i32, (T,))):
+        _cuda_args({"old_lens": (R,), "new_lens": (R,), "free_ring": (None,), "state": (4,),
+                    "state_out": (4,), "cu_new": (R + 1,), "slot_map": (T,)},
+                   dict.fromkeys(("old_lens", "new_lens", "block_table", "free_ring", "state",
+                                  "state_out", "cu_new", "slot_map"), _I32),
+                   old_lens=old_lens, new_lens=new_lens, block_table=block_table,
+                   free_ring=free_ring, state=state, state_out=state_out, cu_new=cu_new,
+                   slot_map=slot_map)
+    _queue(dev, lib().zo_op_block_tables, old_lens.data_ptr(), new_lens.data_ptr(), R, page_size,
+           block_table.data_ptr(), max_blocks, free_ring.data_ptr(), free_ring.shape[0],
+           state.data_ptr(), state_out.data_ptr(), cu_new.data_ptr(), slot_map.data_ptr(), T)
     return cu_new, slot_map
 
 
@@ -787,10 +794,8 @@ def zo_op_kv_write(qkv: torch.Tensor, slot_map: torch.Tensor, cache: torch.Tenso
         _cuda_args({"cache": (None, kv2), "slot_map": (T,)},
                    {"cache": (qkv.dtype,), "slot_map": _I32}, cache=cache, slot_map=slot_map)
         raise ValueError(f"cache and slot_map are on {cache.device}, qkv on {qkv.device}")
-    with _on("qkv", qkv):
-        _check_op(lib().zo_op_kv_write(qkv.data_ptr(), ld, slot_map.data_ptr(), T, cache.data_ptr(),
-                                       slots, n_heads, n_kv_heads, head_dim, _dtype_id(qkv.dtype),
-                                       _raw_stream(dev)))
+    _queue(dev, lib().zo_op_kv_write, qkv.data_ptr(), ld, slot_map.data_ptr(), T, cache.data_ptr(),
+           slots, n_heads, n_kv_heads, head_dim, _dtype_id(qkv.dtype))
 
 
 def zo_op_attention_paged_workspace(n_tokens: int, n_rows: int, n_heads: int, n_kv_heads: int,
@@ -813,30 +818,27 @@ def zo_op_attention_paged(q: torch.Tensor, cache: torch.Tensor, block_table: tor
         raise ValueError("block_table must be [requests x max_blocks]")
     R, max_blocks = block_table.shape
     dt, dev, i32 = q.dtype, q.get_device(), torch.int32
-    with _on("q", q):
-        if out is None:
-            out = torch.empty(T, n_heads * head_dim, dtype=dt, device=q.device)
-        ld_out = _rows("out", out, n_heads * head_dim, (dt,))
-        if out.shape[0] != T or out.get_device() != dev:
-            raise ValueError("out must have q's rows and device")
-        if ws is None:
-            ws = torch.empty(lib().zo_op_attention_paged_workspace(T, R, n_heads, n_kv_heads,
-                                                                   head_dim, _dtype_id(dt)),
-                             dtype=torch.uint8, device=q.device)
-        kv2 = 2 * n_kv_heads * head_dim
-        if not _fits(dev, (cache, dt, (cache.shape[0], kv2)), (block_table, i32, (R, max_blocks)),
-                     (cu_new, i32, (R + 1,)), (lens, i32, (R,)),
-                     (ws, torch.uint8, ws.shape[:1])):
-            _cuda_args({"cache": (None, kv2), "cu_new": (R + 1,), "lens": (R,), "ws": (None,)},
-                       {"cache": (dt,), "block_table": _I32, "cu_new": _I32, "lens": _I32,
-                        "ws": (torch.uint8,)},
-                       cache=cache, block_table=block_table, cu_new=cu_new, lens=lens, ws=ws)
-            raise ValueError(f"cache is on {cache.device}, q on {q.device}")
-        _check_op(lib().zo_op_attention_paged(
-            q.data_ptr(), ld_q, cache.data_ptr(), cache.shape[0], block_table.data_ptr(),
-            max_blocks, page_size, cu_new.data_ptr(), lens.data_ptr(), R, T, max_new, n_heads,
-            n_kv_heads, head_dim, _dtype_id(dt), out.data_ptr(), ld_out, ws.data_ptr(),
-            ws.shape[0], impl, _raw_stream(dev)))
+    did, L = _dtype_id(dt), lib()
+    if out is None:
+        out = torch.empty(T, n_heads * head_dim, dtype=dt, device=q.device)
+    ld_out = _rows("out", out, n_heads * head_dim, (dt,))
+    if out.shape[0] != T or out.get_device() != dev:
+        raise ValueError("out must have q's rows and device")
+    if ws is None:
+        ws = torch.empty(L.zo_op_attention_paged_workspace(T, R, n_heads, n_kv_heads, head_dim, did),
+                         dtype=torch.uint8, device=q.device)
+    kv2 = 2 * n_kv_heads * head_dim
+    if not _fits(dev, (cache, dt, (cache.shape[0], kv2)), (block_table, i32, (R, max_blocks)),
+                 (cu_new, i32, (R + 1,)), (lens, i32, (R,)), (ws, torch.uint8, ws.shape[:1])):
+        _cuda_args({"cache": (None, kv2), "cu_new": (R + 1,), "lens": (R,), "ws": (None,)},
+                   {"cache": (dt,), "block_table": _I32, "cu_new": _I32, "lens": _I32,
+                    "ws": (torch.uint8,)},
+                   cache=cache, block_table=block_table, cu_new=cu_new, lens=lens, ws=ws)
+        raise ValueError(f"cache is on {cache.device}, q on {q.device}")
+    _queue(dev, L.zo_op_attention_paged, q.data_ptr(), ld_q, cache.data_ptr(), cache.shape[0],
+           block_table.data_ptr(), max_blocks, page_size, cu_new.data_ptr(), lens.data_ptr(), R, T,
+           max_new, n_heads, n_kv_heads, head_dim, did, out.data_ptr(), ld_out, ws.data_ptr(),
+           ws.shape[0], impl)
     return out
 
 
@@ -861,31 +863,29 @@ def zo_op_linear_adapters(x: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: 
     rank = A.shape[0] // n_adapters
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    dt, dev, K2 = x.dtype, x.get_device(), n_adapters * rank
-    with _on("x", x):
-        if out is None:
-            out = torch.empty(M, N, dtype=dt, device=x.device)
-        if ws is None:
-            need = lib().zo_op_linear_adapters_workspace(M, N, K, n_adapters, rank, _dtype_id(dt))
-            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
-        f32 = torch.float32
-        if not (dt in _FLOATS and
-                _fits(dev, (x, dt, (M, K)), (W, dt, (N, K)), (A, dt, (K2, K)), (B, dt, (N, K2)),
-                      (row_adapter, torch.int32, (M,)), (scale, f32, (n_adapters,)),
-                      (out, f32 if accumulate else dt, (M, N)), (ws, torch.uint8, ws.shape[:1]))
-                and (bias is None or _fits(dev, (bias, f32, (N,))))):
-            _cuda_args({"x": (M, K), "W": (N, K), "A": (K2, K), "B": (N, K2), "row_adapter": (M,),
-                        "scale": (n_adapters,), "bias": (N,), "out": (M, N), "ws": (None,)},
-                       {"x": _FLOATS, "W": (dt,), "A": (dt,), "B": (dt,), "row_adapter": _I32,
-                        "scale": (f32,), "bias": (f32,), "out": (f32,) if accumulate else (dt,),
-                        "ws": (torch.uint8,)},
-                       x=x, W=W, A=A, B=B, row_adapter=row_adapter, scale=scale, bias=bias,
-                       out=out, ws=ws)
-        _check_op(lib().zo_op_linear_adapters(
-            x.data_ptr(), W.data_ptr(), None if bias is None else bias.data_ptr(), A.data_ptr(),
-            B.data_ptr(), row_adapter.data_ptr(), scale.data_ptr(), n_adapters, rank,
-            out.data_ptr(), M, N, K, _dtype_id(dt), act, int(accumulate), ws.data_ptr(),
-            ws.shape[0], impl, _raw_stream(dev)))
+    dt, dev, K2, f32 = x.dtype, _device_of("x", x), n_adapters * rank, torch.float32
+    did, L = _dtype_id(dt), lib()
+    if out is None:
+        out = torch.empty(M, N, dtype=dt, device=x.device)
+    if ws is None:
+        need = L.zo_op_linear_adapters_workspace(M, N, K, n_adapters, rank, did)
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
+    if not (dt in _FLOATS and
+            _fits(dev, (x, dt, (M, K)), (W, dt, (N, K)), (A, dt, (K2, K)), (B, dt, (N, K2)),
+                  (row_adapter, torch.int32, (M,)), (scale, f32, (n_adapters,)),
+                  (out, f32 if accumulate else dt, (M, N)), (ws, torch.uint8, ws.shape[:1]))
+            and (bias is None or _fits(dev, (bias, f32, (N,))))):
+        _cuda_args({"x": (M, K), "W": (N, K), "A": (K2, K), "B": (N, K2), "row_adapter": (M,),
+                    "scale": (n_adapters,), "bias": (N,), "out": (M, N), "ws": (None,)},
+                   {"x": _FLOATS, "W": (dt,), "A": (dt,), "B": (dt,), "row_adapter": _I32,
+                    "scale": (f32,), "bias": (f32,), "out": (f32,) if accumulate else (dt,),
+                    "ws": (torch.uint8,)},
+                   x=x, W=W, A=A, B=B, row_adapter=row_adapter, scale=scale, bias=bias, out=out,
+                   ws=ws)
+    _queue(dev, L.zo_op_linear_adapters, x.data_ptr(), W.data_ptr(),
+           None if bias is None else bias.data_ptr(), A.data_ptr(), B.data_ptr(),
+           row_adapter.data_ptr(), scale.data_ptr(), n_adapters, rank, out.data_ptr(), M, N, K, did,
+           act, int(accumulate), ws.data_ptr(), ws.shape[0], impl)
     return out
 
 
