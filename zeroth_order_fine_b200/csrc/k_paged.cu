@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(A_THREADS, HD <= 64 ? 2 : 1)
     long long* cum = reinterpret_cast<long long*>(KVs);
     const long long L = Line::prefix(a, A_GROUPS, cum, cum + A_GROUPS + 1);
     const int w = blockIdx.x;
-    const long long stretch = (L + gridDim.x - 1) / gridDim.x;
+    const long long stretch = div_ll(L + gridDim.x - 1, gridDim.x);
     const long long u1 = min(L, stretch * (w + 1));
     long long u = stretch * w;
     if (tid == 0) desc[w].pieces = 0;

@@ -337,11 +337,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     long long* wsum = cum + GROUPS + 1;
     const long long L = Line::prefix(a, GROUPS, cum, wsum);
     const int w = blockIdx.x;
-    const long long stretch = (L + gridDim.x - 1) / gridDim.x;
+    const long long stretch = div_ll(L + gridDim.x - 1, gridDim.x);
     const long long u0 = stretch * w, u1 = min(L, u0 + stretch);
     if (tid == 0) desc[w].pieces = 0;
     if (u0 >= u1) return;                             // the whole CTA
-    if (tid == 0) *first = Line::locate(a, GROUPS, cum, u0);
+    if (warp == 0) {
+        const Line::Cursor k = Line::locate(a, GROUPS, cum, u0);
+        if (lane == 0) *first = k;
+    }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tslot))
                      : "memory");

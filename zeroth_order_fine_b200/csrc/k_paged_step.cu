@@ -107,6 +107,10 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<uint32_t*>(&h);
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 // Slots of partial results, in the accumulator's own layout: slot 2 w: the piece with which team
 // w's stretch begins (an item begun by an earlier team); 2 w + 1: the one it ends with (an item
 // that goes on); each with a part per warp of the team.  desc[w] describes the item of slot
@@ -156,46 +160,75 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int s = 0; s < STAGES; ++s)
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar0 + 8u * s));
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (tid == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
     grid_dep_launch();                                // the joining kernel may be scheduled
 
+    // The tables and the queries into L2, a line per thread over the grid: both are read where the
+    // copies and the products would wait for DRAM.
+    {
+        const long long i = (long long)blockIdx.x * THREADS + tid;
+        if (i < ((long long)a.n_rows * a.max_blocks + 31) / 32) prefetch_l2(a.block_table + i * 32);
+        const int per_row = (a.g * a.Hkv * HD + 63) / 64;
+        if (i < (long long)a.n_tokens * per_row) {
+            const int t = (int)((unsigned)i / (unsigned)per_row);
+            prefetch_l2(static_cast<const __nv_bfloat16*>(a.q) + (size_t)t * a.ld_q + ((int)i - t * per_row) * 64);
+        }
+    }
     using Line = PagedLine<false, RB, UK>;
     const long long L = Line::prefix(a, GROUPS, cum, wsum);
     const int team = min(WARPS, a.Hkv & -a.Hkv);      // a power of two, as WARPS is
     const int workers = gridDim.x * (WARPS / team), w = blockIdx.x * (WARPS / team) + warp / team;
     const int mate = warp % team;                     // the warp's head within the team's
-    const long long stretch = (L + workers - 1) / workers;      // units per worker
+    const long long stretch = div_ll(L + workers - 1, workers);      // units per worker
     const long long u0 = stretch * w, u1 = min(L, u0 + stretch);
     if (mate == 0 && lane == 0) desc[w].pieces = 0;
     if (u0 >= u1) return;                             // nothing to do, nothing in flight
 
-    typename Line::Cursor con = Line::locate(a, GROUPS, cum, u0);
-    typename Line::Cursor pro = con;
+    const int count = (int)(u1 - u0);                 // units of this stretch
+    struct Place {
+        typename Line::Cursor c;
+        int kend;                                     // the tile's keys
+    };
+    Place con;
+    con.c = Line::locate(a, GROUPS, cum, u0);
+    con.kend = Line::keys(a, con.c.q, (con.c.tile + 1) * RB);
+    Place pro = con;
+    // to the next unit; true: it belongs to another tile.  `more`: the stretch goes on
+    auto advance = [&](Place& p, bool more) {
+        if (++p.c.unit < p.c.units) return false;
+        p.c.unit = 0;
+        if (++p.c.head < a.line_heads) return false;
+        p.c.head = 0;
+        if (!more) return false;
+        Line::next_tile(a, p.c);
+        p.kend = Line::keys(a, p.c.q, (p.c.tile + 1) * RB);
+        return true;
+    };
 
     // ---- producer side of the warp: unit `pro` into stage ps ----
     const int n_pages = (int)(a.n_slots >> a.page_shift);
     int ids = 0, ids_at = -1, ids_r = -1;             // 32 table entries, one per lane
     uint32_t bad_stage = 0;
     auto page_of = [&](int idx) {
-        if (ids_r != pro.r || idx < ids_at || idx >= ids_at + 32) {
-            ids_r = pro.r;
+        if (ids_r != pro.c.r || idx < ids_at || idx >= ids_at + 32) {
+            ids_r = pro.c.r;
             ids_at = idx;
-            ids = idx + lane < a.max_blocks ? a.block_table[(size_t)pro.r * a.max_blocks + idx + lane] : -1;
+            ids = idx + lane < a.max_blocks ? a.block_table[(size_t)pro.c.r * a.max_blocks + idx + lane] : -1;
         }
         return __shfl_sync(0xffffffffu, ids, idx - ids_at);
     };
     auto issue = [&](int ps) {
         const uint32_t dst = ring + (uint32_t)(ps * G::STAGE), bar = bar0 + 8u * ps;
-        const int kbase = pro.unit * UK;
+        const int kbase = pro.c.unit * UK;
         uint32_t bytes = 0;
         int row[2] = {-1, -1};
-        bool bad = pro.q.bad;
+        bool bad = pro.c.q.bad;
         if (!bad) {
-            const int kend = Line::keys(a, pro.q, (pro.tile + 1) * RB);
             const int subs = UK / box_rows;           // boxes per unit: 1, or 2 with pages of 8
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const int k = kbase + s * box_rows;
-                if (s < subs && k < kend) {
+                if (s < subs && k < pro.kend) {
                     const int page = page_of(k >> a.page_shift);
                     if ((unsigned)page < (unsigned)n_pages) {
                         row[s] = (page << a.page_shift) + (k & ((1 << a.page_shift) - 1));
@@ -217,15 +250,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
                         " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst + (uint32_t)(s * box_rows * HD * 4)),
                         "l"(reinterpret_cast<uint64_t>(&map)), "r"(bar), "r"(0), "r"(row[s]),
-                        "r"((pro.head * team + mate) * NH), "r"(0)
+                        "r"((pro.c.head * team + mate) * NH), "r"(0)
                         : "memory");
         }
     };
-    long long issued = u0;
-    for (int s = 0; s < STAGES && issued < u1; ++s) {
+    int issued = 0;
+    for (int s = 0; s < STAGES && issued < count; ++s) {
         issue(s);
         ++issued;
-        Line::advance(a, pro, 1, issued < u1);
+        advance(pro, issued < count);
     }
 
     // ---- consumer side ----
@@ -240,35 +273,49 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t k_chunk = lane >> 4, v_chunk = (lane >> 3) & 1, swz = lane & 7;
 
     uint32_t qf[HD / 16][NB][2];
-    float o[HD / 16][NB][4], m[NB][2], l[NB][2];
-    int lim[NB][2], kend = 0, first_unit = 0;
-    bool bad = false, fresh = true, alive = true;
+    float o[HD / 16][NB][4], m[NB][2], l[NB][2];      // m in units of ln 2 of the scaled scores
+    int lim[NB][2], lim_min = 0, first_unit = 0;
+    size_t q_at[NB], out_at[NB][2];                   // the lane's query and output rows, head 0
+    uint32_t q_live = 0;
+    bool bad = false, fresh = true, new_tile = true, alive = true;
     int stage = 0;
     uint32_t phase = 0;
-    for (long long u = u0; u < u1; ++u) {
-        if (fresh) {                                  // a new item: its query rows and masks
-            fresh = false;
-            first_unit = con.unit;
-            bad = con.q.bad;
-            kend = Line::keys(a, con.q, (con.tile + 1) * RB);
-            const int row0 = con.tile * RB;
+    for (int u = 0; u < count; ++u) {
+        if (new_tile) {                               // the tile's rows and masks
+            new_tile = false;
+            const int row0 = con.c.tile * RB;
+            lim_min = con.c.q.bad ? 0 : con.c.q.ctx + row0 / a.g + 1;
+            q_live = 0;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 const int row = row0 + nb * 8 + (lane >> 2);
-                const bool live = row < con.q.rows;
-                const int rr = live ? row : row0;
+                const int rr = row < con.c.q.rows ? row : row0;
+                if (row < con.c.q.rows) q_live |= 1u << nb;
+                q_at[nb] = (size_t)(con.c.q.start + rr / a.g) * a.ld_q + (size_t)(rr % a.g) * HD + 2 * (lane & 3);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int n = row0 + nb * 8 + 2 * (lane & 3) + e, nr = min(n, con.c.q.rows - 1);
+                    lim[nb][e] = n < con.c.q.rows ? con.c.q.ctx + nr / a.g + 1 : con.kend;
+                    out_at[nb][e] = (size_t)(con.c.q.start + nr / a.g) * a.ld_out + (size_t)(nr % a.g) * HD + (lane >> 2);
+                }
+            }
+        }
+        if (fresh) {                                  // a new item: its queries
+            fresh = false;
+            first_unit = con.c.unit;
+            bad = con.c.q.bad;
+            const size_t head = (size_t)((con.c.head * team + mate) * a.g) * HD;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
                 const uint32_t* q = reinterpret_cast<const uint32_t*>(
-                    static_cast<const __nv_bfloat16*>(a.q) + (size_t)(con.q.start + rr / a.g) * a.ld_q +
-                    (size_t)((con.head * team + mate) * a.g + rr % a.g) * HD + 2 * (lane & 3));
+                    static_cast<const __nv_bfloat16*>(a.q) + q_at[nb] + head);
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk) {
-                    qf[kk][nb][0] = live ? __ldg(q + kk * 8) : 0u;
-                    qf[kk][nb][1] = live ? __ldg(q + kk * 8 + 4) : 0u;
+                    qf[kk][nb][0] = (q_live >> nb) & 1u ? __ldg(q + kk * 8) : 0u;
+                    qf[kk][nb][1] = (q_live >> nb) & 1u ? __ldg(q + kk * 8 + 4) : 0u;
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int n = row0 + nb * 8 + 2 * (lane & 3) + e;
-                    lim[nb][e] = n < con.q.rows ? con.q.ctx + n / a.g + 1 : kend;
                     m[nb][e] = -FLT_MAX;
                     l[nb][e] = 0.f;
                 }
@@ -286,55 +333,67 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         bad |= (bad_stage >> stage) & 1u;
         const uint32_t at = ring + (uint32_t)(stage * G::STAGE);
-        const int kbase = con.unit * UK;
-        float s[NB][4];
+        const int kbase = con.c.unit * UK;
+        float s[NB][4], s1[NB][4];                    // two chains of products
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[nb][e] = 0.f;
+            for (int e = 0; e < 4; ++e) s[nb][e] = s1[nb][e] = 0.f;
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk) {
             uint32_t kf[4];
             const uint32_t ch = (kk & 3) * 2 + k_chunk;
             ldsm4(kf, at + k_row + (kk >> 2) * half_st + ((ch ^ swz) << 4));
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma16816(s[nb], kf, qf[kk][nb]);
+            for (int nb = 0; nb < NB; ++nb) mma16816(kk & 1 ? s1[nb] : s[nb], kf, qf[kk][nb]);
         }
-        const int left = kend - kbase;                // keys of the unit that exist for the tile
+        const int left = con.kend - kbase;            // keys of the unit that exist for the tile
         uint32_t pf[NB][2];
-        bool moved = false;
-        float alpha[NB][2];
+        bool move = false;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[nb][e] = (s[nb][e] + s1[nb][e]) * sl2;
+        if (kbase + UK > lim_min) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = kbase + (lane >> 2) + (e >> 1) * 8;
+                    if (key >= min(lim[nb][e & 1], con.kend)) s[nb][e] = -INFINITY;
+                }
+        }
+        // a row's reference moves only when a score is over 2^8 above it: then to the row's maximum
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) move |= fmaxf(s[nb][e], s[nb][e + 2]) > m[nb][e] + 8.f;
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(s[nb][e], s[nb][e + 2]);
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                    const float mn = fmaxf(m[nb][e], mx), f = ex2(m[nb][e] - mn);
+                    m[nb][e] = mn;
+                    l[nb][e] *= f;
+#pragma unroll
+                    for (int mt = 0; mt < HD / 16; ++mt) {
+                        o[mt][nb][e] *= f;
+                        o[mt][nb][e + 2] *= f;
+                    }
+                }
+        }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int key = kbase + (lane >> 2) + (e >> 1) * 8;
-                if (key >= min(lim[nb][e & 1], kend)) s[nb][e] = -INFINITY;
-            }
+            for (int e = 0; e < 4; ++e) s[nb][e] = ex2(s[nb][e] - m[nb][e & 1]);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float mx = fmaxf(s[nb][e], s[nb][e + 2]);
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                const float mn = fmaxf(m[nb][e], mx);
-                alpha[nb][e] = ex2((m[nb][e] - mn) * sl2);
-                moved |= mn > m[nb][e];
-                m[nb][e] = mn;
-                const float ms = mn * sl2;
-                s[nb][e] = ex2(fmaf(s[nb][e], sl2, -ms));
-                s[nb][e + 2] = ex2(fmaf(s[nb][e + 2], sl2, -ms));
-                l[nb][e] = l[nb][e] * alpha[nb][e] + (s[nb][e] + s[nb][e + 2]);
-            }
+            for (int e = 0; e < 2; ++e) l[nb][e] += s[nb][e] + s[nb][e + 2];
             pf[nb][0] = transpose8x8(pack2(s[nb][0], s[nb][1]));
             pf[nb][1] = transpose8x8(pack2(s[nb][2], s[nb][3]));
-        }
-        if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-            for (int mt = 0; mt < HD / 16; ++mt)
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[mt][nb][e] *= alpha[nb][e & 1];
         }
         // value rows behind the last key: cleared, the two keys of a register one by one
         const int k2 = 2 * (lane & 3);
@@ -355,18 +414,18 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int nb = 0; nb < NB; ++nb) mma16816(o[mt][nb], vf, pf[nb]);
         }
         __syncwarp();                                 // every lane has read the stage
-        if (issued < u1) {
+        if (issued < count) {
             issue(stage);
             ++issued;
-            Line::advance(a, pro, 1, issued < u1);
+            advance(pro, issued < count);
         }
         if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
         }
 
-        const bool item_end = con.unit + 1 == con.units;
-        if (item_end || u + 1 == u1) {
+        const bool item_end = con.c.unit + 1 == con.c.units;
+        if (item_end || u + 1 == count) {
             fresh = true;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
@@ -376,14 +435,21 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int d = 4; d < 32; d <<= 1) l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], d);
                     if (bad) l[nb][e] = __int_as_float(0x7fc00000);
                 }
-            const int row0 = con.tile * RB, rows = min(RB, con.q.rows - row0);
+            const int row0 = con.c.tile * RB, rows = min(RB, con.c.q.rows - row0);
             if (first_unit == 0 && item_end) {
-                float inv[NB][2];
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (size_t)((con.c.head * team + mate) * a.g) * HD;
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) inv[nb][e] = 1.f / l[nb][e];
-                store_rows<HD, NB, HD / 16>(a, con.q.start, row0, rows, con.head * team + mate, 0, o, inv, lane);
+                    for (int e = 0; e < 2; ++e) {
+                        if (nb * 8 + 2 * (lane & 3) + e >= rows) continue;
+                        const float inv = 1.f / l[nb][e];
+#pragma unroll
+                        for (int mt = 0; mt < HD / 16; ++mt) {
+                            out[out_at[nb][e] + mt * 16] = __float2bfloat16_rn(o[mt][nb][e] * inv);
+                            out[out_at[nb][e] + mt * 16 + 8] = __float2bfloat16_rn(o[mt][nb][2 + e] * inv);
+                        }
+                    }
             } else {
                 Part<HD, NB>& p = part[(2 * w + (first_unit == 0 ? 1 : 0)) * team + mate];
 #pragma unroll
@@ -401,25 +467,25 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                 if (first_unit == 0 && mate == 0 && lane == 0) {
                     // the item's last unit is (units - 1) behind its first, which is u - unit
-                    const long long last = u - con.unit + con.units - 1;
+                    const long long last = u0 + u - con.c.unit + con.c.units - 1;
                     PagedDesc d;
-                    d.pieces = (int)(last / stretch) - w + 1;
-                    d.start = con.q.start;
+                    d.pieces = (int)div_ll(last, stretch) - w + 1;
+                    d.start = con.c.q.start;
                     d.row0 = row0;
                     d.rows = rows;
-                    d.kvh = con.head * team;
+                    d.kvh = con.c.head * team;
                     desc[w] = d;
                 }
             }
         }
-        Line::advance(a, con, 1, u + 1 < u1);
+        new_tile = advance(con, u + 1 < count);
     }
     if (!alive) {
         // the copies still in flight land (or the bound ends) before the memory goes away
-        const int n = (int)min((long long)STAGES, issued - u0);
+        const int n = min(STAGES, issued);
         for (int s = 0; s < n; ++s) {
-            const uint32_t ph = (uint32_t)(((issued - u0 - 1 - s) / STAGES) & 1);
-            const uint32_t bar = bar0 + 8u * (uint32_t)((issued - u0 - 1 - s) % STAGES);
+            const uint32_t ph = (uint32_t)(((issued - 1 - s) / STAGES) & 1);
+            const uint32_t bar = bar0 + 8u * (uint32_t)((issued - 1 - s) % STAGES);
             for (uint32_t i = 0; i < DRAIN_POLLS && !bar_try(bar, ph); ++i) __nanosleep(128);
         }
     }
@@ -439,7 +505,6 @@ __global__ void __launch_bounds__(128) paged_step_join_kernel(PagedArgs a, const
     const int w = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const PagedDesc d = desc[w];
     if (d.pieces <= 0) return;
-    const float sl2 = a.scale * 1.4426950408889634f;
     const int c = 2 * (lane & 3);
     float o[MT][NB][4], m[NB][2], l[NB][2];
 #pragma unroll
@@ -471,7 +536,7 @@ __global__ void __launch_bounds__(128) paged_step_join_kernel(PagedArgs a, const
             for (int e = 0; e < 2; ++e) {
                 float mn = m[nb][e];
                 for (int i = 0; i < n; ++i) mn = fmaxf(mn, sm[i][nb * 8 + c + e]);
-                const float f = ex2((m[nb][e] - mn) * sl2);
+                const float f = ex2(m[nb][e] - mn);
                 l[nb][e] *= f;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
@@ -488,7 +553,7 @@ __global__ void __launch_bounds__(128) paged_step_join_kernel(PagedArgs a, const
                 float f[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    f[e] = ex2((sm[i][nb * 8 + c + e] - m[nb][e]) * sl2);
+                    f[e] = ex2(sm[i][nb * 8 + c + e] - m[nb][e]);
                     l[nb][e] = fmaf(f[e], sl[i][nb * 8 + c + e], l[nb][e]);
                 }
 #pragma unroll

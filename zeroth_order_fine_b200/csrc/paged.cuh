@@ -9,6 +9,11 @@
 
 namespace zo {
 
+// a / b for a >= 0, b > 0: a 32-bit division wherever that does (a 64-bit one is ~5 times slower)
+__device__ __forceinline__ long long div_ll(long long a, long long b) {
+    return ((a | b) >> 32) ? a / b : (long long)((unsigned)a / (unsigned)b);
+}
+
 // A kernel takes the requests of at most step_tokens new tokens (BIG false) or the others (BIG
 // true); the rest have no rows for it.  RB query rows (new tokens x g of one kv head) make a tile,
 // UK keys a unit; a place on the line stands for line_heads-th parts of the kv heads.
@@ -82,15 +87,17 @@ struct PagedLine {
         __syncthreads();
         return base;
     }
-    // The place of unit u (below the total).
+    // The place of unit u (below the total); a whole warp calls it with the same u, max_groups <= 1024.
     static __device__ __forceinline__ Cursor locate(const PagedArgs& a, int max_groups,
                                                     const long long* cum, long long u) {
         const int c = (a.n_rows + max_groups - 1) / max_groups;
-        int lo = 0, hi = (a.n_rows + c - 1) / c;       // the last group with cum <= u
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (cum[mid] <= u) lo = mid;
-            else hi = mid;
+        const int groups = (a.n_rows + c - 1) / c, lane = threadIdx.x & 31;
+        int lo = 0;                                    // the last group with cum <= u
+        for (int step = groups > 32 ? 32 : 1;; step >>= 5) {
+            const int at = lo + lane * step;
+            const unsigned le = __ballot_sync(0xffffffffu, at < groups && cum[at] <= u);
+            lo += (31 - __clz(le)) * step;             // cum does not fall: the bits set are the low ones
+            if (step == 1) break;
         }
         long long rest = u - cum[lo];
         Cursor k;
@@ -110,8 +117,8 @@ struct PagedLine {
             rest -= n;
             ++k.tile;
         }
-        k.head = (int)(rest / k.units);
-        k.unit = (int)(rest % k.units);
+        k.head = (int)div_ll(rest, k.units);
+        k.unit = (int)(rest - (long long)k.head * k.units);
         return k;
     }
     // On by n units of the same (request, tile, head), n <= units - unit; `more`: the line goes on
@@ -122,7 +129,10 @@ struct PagedLine {
         k.unit = 0;
         if (++k.head < a.line_heads) return;
         k.head = 0;
-        if (!more) return;
+        if (more) next_tile(a, k);
+    }
+    // To the next tile, of the next request that has rows here if need be (there is one).
+    static __device__ __forceinline__ void next_tile(const PagedArgs& a, Cursor& k) {
         if (++k.tile * RB >= k.q.rows) {
             k.tile = 0;
             do {
