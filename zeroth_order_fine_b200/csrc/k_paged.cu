@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(A_THREADS, HD <= 64 ? 2 : 1)
             const int q = i / HD, d = i % HD;
             float v = 0.f;
             if (q < rows) {
-                const int t = (row0 + q) / a.g, h = kvh * a.g + (row0 + q) % a.g;
+                const int t = by_g(a, row0 + q), h = kvh * a.g + mod_g(a, row0 + q);
                 v = ld_elem(a.q, (size_t)(k.q.start + t) * a.ld_q + (size_t)h * HD + d, a.dtype) * sl2;
             }
             Qs[q * LD + d] = v;
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(A_THREADS, HD <= 64 ? 2 : 1)
         for (int i = 0; i < RT; ++i) {
             m[i] = -FLT_MAX;
             l[i] = 0.f;
-            lim[i] = min(kend, k.q.ctx + (row0 + RT * ty + i) / a.g + 1);
+            lim[i] = min(kend, k.q.ctx + by_g(a, row0 + RT * ty + i) + 1);
 #pragma unroll
             for (int d = 0; d < NV; ++d)
 #pragma unroll
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(A_THREADS, HD <= 64 ? 2 : 1)
                 p[AQ * HD + q] = m[i];
                 p[AQ * HD + AQ + q] = l[i];
             }
-            const int t = (row0 + q) / a.g, h = kvh * a.g + (row0 + q) % a.g;
+            const int t = by_g(a, row0 + q), h = kvh * a.g + mod_g(a, row0 + q);
             const size_t out = (size_t)(k.q.start + t) * a.ld_out + (size_t)h * HD;
             const float inv = 1.f / l[i];
 #pragma unroll
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(A_THREADS)
             o[0] = fmaf(f, v.x, o[0]); o[1] = fmaf(f, v.y, o[1]);
             o[2] = fmaf(f, v.z, o[2]); o[3] = fmaf(f, v.w, o[3]);
         }
-        const int tok = (t.row0 + q) / a.g, h = t.kvh * a.g + (t.row0 + q) % a.g;
+        const int tok = by_g(a, t.row0 + q), h = t.kvh * a.g + mod_g(a, t.row0 + q);
         for (int e = 0; e < 4; ++e)
             st_elem(a.out, (size_t)(t.start + tok) * a.ld_out + (size_t)h * HD + d + e, a.dtype, o[e] / l);
     }

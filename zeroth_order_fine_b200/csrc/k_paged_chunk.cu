@@ -500,8 +500,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool live = r < at.q.rows;
             const int rr = live ? r : 0;
             const uint4* q = reinterpret_cast<const uint4*>(
-                static_cast<const __nv_bfloat16*>(a.q) + (size_t)(at.q.start + rr / a.g) * a.ld_q +
-                (size_t)(at.head * a.g + rr % a.g) * HD);
+                static_cast<const __nv_bfloat16*>(a.q) + (size_t)(at.q.start + by_g(a, rr)) * a.ld_q +
+                (size_t)(at.head * a.g + mod_g(a, rr)) * HD);
 #pragma unroll 8
             for (int ch = 0; ch < HD / 8; ++ch)
                 *reinterpret_cast<uint4*>(qs + (ch >> 3) * ATOM + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) =
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int r = it.tile * RB + t * 128 + row;
             const bool live = r < it.q.rows;
             // keys below lim are seen by this row
-            const int lim = it.q.bad || !live ? 0 : it.q.ctx + r / a.g + 1;
+            const int lim = it.q.bad || !live ? 0 : it.q.ctx + by_g(a, r) + 1;
             const int e = p.end(t);
             const uint64_t c2 = pair(sl2, sl2);
             for (int c = p.c0; c < e; ++c) {
@@ -650,8 +650,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 fence_after();
                 const float inv = 1.f / lt;
                 __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
-                                     (size_t)(it.q.start + r / a.g) * a.ld_out +
-                                     (size_t)(it.head * a.g + r % a.g) * HD;
+                                     (size_t)(it.q.start + by_g(a, r)) * a.ld_out +
+                                     (size_t)(it.head * a.g + mod_g(a, r)) * HD;
 #pragma unroll 1
                 for (int j = 0; j < HD / 32; ++j) {
                     uint32_t v[32];
@@ -749,8 +749,8 @@ __global__ void __launch_bounds__(JOIN_THREADS)
     const float inv = 1.f / l;
     const int q = d.row0 + row;
     uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) +
-                                          (size_t)(d.start + q / a.g) * a.ld_out +
-                                          (size_t)(d.kvh * a.g + q % a.g) * HD) + dg * DG;
+                                          (size_t)(d.start + by_g(a, q)) * a.ld_out +
+                                          (size_t)(d.kvh * a.g + mod_g(a, q)) * HD) + dg * DG;
 #pragma unroll
     for (int j = 0; j < DG; ++j)
         out[j] = make_uint2(pack2(o[j].x * inv, o[j].y * inv), pack2(o[j].z * inv, o[j].w * inv));

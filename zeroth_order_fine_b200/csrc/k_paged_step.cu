@@ -133,8 +133,8 @@ __device__ __forceinline__ void store_rows(const PagedArgs& a, int start, int ro
             if (n >= rows) continue;
             const int row = row0 + n;
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
-                                 (size_t)(start + row / a.g) * a.ld_out +
-                                 (size_t)(kvh * a.g + row % a.g) * HD + mt0 * 16 + (lane >> 2);
+                                 (size_t)(start + by_g(a, row)) * a.ld_out +
+                                 (size_t)(kvh * a.g + mod_g(a, row)) * HD + mt0 * 16 + (lane >> 2);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 out[mt * 16] = __float2bfloat16_rn(o[mt][nb][e] * inv[nb][e]);
@@ -284,19 +284,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (new_tile) {                               // the tile's rows and masks
             new_tile = false;
             const int row0 = con.c.tile * RB;
-            lim_min = con.c.q.bad ? 0 : con.c.q.ctx + row0 / a.g + 1;
+            lim_min = con.c.q.bad ? 0 : con.c.q.ctx + by_g(a, row0) + 1;
             q_live = 0;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 const int row = row0 + nb * 8 + (lane >> 2);
                 const int rr = row < con.c.q.rows ? row : row0;
                 if (row < con.c.q.rows) q_live |= 1u << nb;
-                q_at[nb] = (size_t)(con.c.q.start + rr / a.g) * a.ld_q + (size_t)(rr % a.g) * HD + 2 * (lane & 3);
+                q_at[nb] = (size_t)(con.c.q.start + by_g(a, rr)) * a.ld_q + (size_t)(mod_g(a, rr)) * HD + 2 * (lane & 3);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int n = row0 + nb * 8 + 2 * (lane & 3) + e, nr = min(n, con.c.q.rows - 1);
-                    lim[nb][e] = n < con.c.q.rows ? con.c.q.ctx + nr / a.g + 1 : con.kend;
-                    out_at[nb][e] = (size_t)(con.c.q.start + nr / a.g) * a.ld_out + (size_t)(nr % a.g) * HD + (lane >> 2);
+                    lim[nb][e] = n < con.c.q.rows ? con.c.q.ctx + by_g(a, nr) + 1 : con.kend;
+                    out_at[nb][e] = (size_t)(con.c.q.start + by_g(a, nr)) * a.ld_out + (size_t)(mod_g(a, nr)) * HD + (lane >> 2);
                 }
             }
         }

@@ -217,6 +217,11 @@ struct PagedArgs {
     int dtype;
     void* out; long long ld_out;
     void* ws;
+    // x / g = x * g_mul >> g_shift for 0 <= x < 2^31: with 2^b the power of two at or above g, g_shift
+    // = 31 + b and g_mul = ceil(2^g_shift / g) <= 2^32, which is over by less than 1, so the quotient
+    // is over by less than x / 2^g_shift <= 1 / g before the floor
+    unsigned long long g_mul;
+    int g_shift;
     int line_heads;                         // groups of kv heads on a kernel's line of work
     int step_tokens;                        // requests of at most so many new tokens take the
                                             // decode-step kernel

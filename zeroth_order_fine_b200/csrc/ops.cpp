@@ -365,6 +365,8 @@ int zo_op_attention_paged(const void* q, int64_t ld_q, const void* cache, int64_
     a.cu_new = cu_new; a.lens = lens;
     a.n_rows = n_rows; a.n_tokens = n_tokens; a.max_new = max_new;
     a.H = n_heads; a.Hkv = n_kv_heads; a.g = n_heads / n_kv_heads; a.hd = head_dim;
+    for (a.g_shift = 31; (1ll << (a.g_shift - 31)) < a.g;) ++a.g_shift;
+    a.g_mul = ((1ull << a.g_shift) + a.g - 1) / a.g;
     a.scale = (float)(1.0 / std::sqrt((double)head_dim));
     a.dtype = dtype == ZO_DTYPE_BF16 ? E_BF16 : E_F32;
     a.out = out; a.ld_out = ld_out;

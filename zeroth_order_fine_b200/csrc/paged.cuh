@@ -14,6 +14,12 @@ __device__ __forceinline__ long long div_ll(long long a, long long b) {
     return ((a | b) >> 32) ? a / b : (long long)((unsigned)a / (unsigned)b);
 }
 
+// a row's token (x / g) and its head of the group
+__device__ __forceinline__ int by_g(const PagedArgs& a, int x) {
+    return (int)((unsigned long long)(unsigned)x * a.g_mul >> a.g_shift);
+}
+__device__ __forceinline__ int mod_g(const PagedArgs& a, int x) { return x - by_g(a, x) * a.g; }
+
 // A kernel takes the requests of at most step_tokens new tokens (BIG false) or the others (BIG
 // true); the rest have no rows for it.  RB query rows (new tokens x g of one kv head) make a tile,
 // UK keys a unit; a place on the line stands for line_heads-th parts of the kv heads.
@@ -42,7 +48,7 @@ struct PagedLine {
     }
     // keys that the rows before `end` of a request see, and units of its tile t
     static __device__ __forceinline__ int keys(const PagedArgs& a, const Req& q, int end) {
-        return q.bad ? 0 : q.ctx + (min(end, q.rows) - 1) / a.g + 1;
+        return q.bad ? 0 : q.ctx + by_g(a, min(end, q.rows) - 1) + 1;
     }
     static __device__ __forceinline__ int units(const PagedArgs& a, const Req& q, int t) {
         return q.bad ? 1 : (keys(a, q, (t + 1) * RB) + UK - 1) / UK;
@@ -59,7 +65,7 @@ struct PagedLine {
                                                        long long* wsum) {
         const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = blockDim.x >> 5;
         const int c = (a.n_rows + max_groups - 1) / max_groups;
-        const int groups = (a.n_rows + c - 1) / c;
+        const int groups = c == 1 ? a.n_rows : (a.n_rows + c - 1) / c;
         long long base = 0;
         for (int g0 = 0; g0 < groups; g0 += blockDim.x) {
             const int gi = g0 + tid;
@@ -91,7 +97,7 @@ struct PagedLine {
     static __device__ __forceinline__ Cursor locate(const PagedArgs& a, int max_groups,
                                                     const long long* cum, long long u) {
         const int c = (a.n_rows + max_groups - 1) / max_groups;
-        const int groups = (a.n_rows + c - 1) / c, lane = threadIdx.x & 31;
+        const int groups = c == 1 ? a.n_rows : (a.n_rows + c - 1) / c, lane = threadIdx.x & 31;
         int lo = 0;                                    // the last group with cum <= u
         for (int step = groups > 32 ? 32 : 1;; step >>= 5) {
             const int at = lo + lane * step;
