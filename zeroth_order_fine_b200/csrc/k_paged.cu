@@ -3,6 +3,8 @@
 // sizes the tensor-core kernels do not take).
 #include <float.h>
 
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace zo {
@@ -259,7 +261,10 @@ __global__ void __launch_bounds__(A_THREADS, HD <= 64 ? 2 : 1)
             }
         };
         if (STAGES > 1) load(first);
-        for (int i = tid; i < AQ * HD; i += A_THREADS) {
+        // few rows: 2 or 4 groups of warps, each with all rows and its part of every chunk's keys
+        const int groups = rows > AQ / 2 ? 1 : rows > AQ / 4 ? 2 : 4, span = AQ / groups;
+        const int kg = ty * RT / span, r0 = RT * ty - kg * span;      // the thread's keys and rows
+        for (int i = tid; i < span * HD; i += A_THREADS) {
             const int q = i / HD, d = i % HD;
             float v = 0.f;
             if (q < rows) {
@@ -275,46 +280,41 @@ __global__ void __launch_bounds__(A_THREADS, HD <= 64 ? 2 : 1)
         for (int i = 0; i < RT; ++i) {
             m[i] = -FLT_MAX;
             l[i] = 0.f;
-            lim[i] = min(kend, k.q.ctx + by_g(a, row0 + RT * ty + i) + 1);
+            lim[i] = min(kend, k.q.ctx + by_g(a, row0 + r0 + i) + 1);
 #pragma unroll
             for (int d = 0; d < NV; ++d)
 #pragma unroll
                 for (int e = 0; e < VW / 2; ++e) o[i][d][e] = 0ull;
         }
         // a warp's rows past the tile's take no part in the products
-        const bool warp_live = 2 * RT * (tid >> 5) < rows;
+        const bool warp_live = (r0 & ~(2 * RT - 1)) < rows;
 
-        for (int c = first; c < chunks; ++c) {
-            if (STAGES == 1) {
-                __syncthreads();
-                load(c);
-            }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            __syncthreads();               // chunk c is there; chunk c - 1 has been read
-            if (STAGES > 1 && c + 1 < chunks) load(c + 1);
+        // a chunk for the thread's 16 NJ keys
+        auto attend = [&](int c, auto nj) {
+            constexpr int NJ = decltype(nj)::value;
+            const int key0 = 16 * NJ * kg;
             const float* Ks = KVs + (size_t)(c % STAGES) * 2 * AK * LD;
             const float* Vs = Ks + AK * LD;
-            if (!warp_live) continue;
-            float s[RT][4];
+            float s[RT][NJ];
             {
-                uint64_t s2[RT][4];        // sums over the even and over the odd dims
+                uint64_t s2[RT][NJ];        // sums over the even and over the odd dims
 #pragma unroll
                 for (int i = 0; i < RT; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) s2[i][j] = 0ull;
+                    for (int j = 0; j < NJ; ++j) s2[i][j] = 0ull;
 #pragma unroll 4
                 for (int d = 0; d < HD; d += 4) {
-                    ulonglong2 qv[RT], kv[4];
+                    ulonglong2 qv[RT], kv[NJ];
 #pragma unroll
                     for (int i = 0; i < RT; ++i)
-                        qv[i] = *reinterpret_cast<const ulonglong2*>(Qs + (RT * ty + i) * LD + d);
+                        qv[i] = *reinterpret_cast<const ulonglong2*>(Qs + (r0 + i) * LD + d);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        kv[j] = *reinterpret_cast<const ulonglong2*>(Ks + (tx + 16 * j) * LD + d);
+                    for (int j = 0; j < NJ; ++j)
+                        kv[j] = *reinterpret_cast<const ulonglong2*>(Ks + (key0 + tx + 16 * j) * LD + d);
 #pragma unroll
                     for (int i = 0; i < RT; ++i)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
+                        for (int j = 0; j < NJ; ++j) {
                             fma_pair(s2[i][j], qv[i].x, kv[j].x);
                             fma_pair(s2[i][j], qv[i].y, kv[j].y);
                         }
@@ -322,15 +322,15 @@ __global__ void __launch_bounds__(A_THREADS, HD <= 64 ? 2 : 1)
 #pragma unroll
                 for (int i = 0; i < RT; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) s[i][j] = half_of(s2[i][j], 0) + half_of(s2[i][j], 1);
+                    for (int j = 0; j < NJ; ++j) s[i][j] = half_of(s2[i][j], 0) + half_of(s2[i][j], 1);
             }
 #pragma unroll
             for (int i = 0; i < RT; ++i) {
-                bool see[4];
+                bool see[NJ];
                 float mx = -FLT_MAX;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    see[j] = c * AK + tx + 16 * j < lim[i];
+                for (int j = 0; j < NJ; ++j) {
+                    see[j] = c * AK + key0 + tx + 16 * j < lim[i];
                     if (see[j]) mx = fmaxf(mx, s[i][j]);
                 }
 #pragma unroll
@@ -339,10 +339,10 @@ __global__ void __launch_bounds__(A_THREADS, HD <= 64 ? 2 : 1)
                 const float corr = ex2(m[i] - mn);
                 float sum = 0.f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < NJ; ++j) {
                     const float p = see[j] ? ex2(s[i][j] - mn) : 0.f;
                     sum += p;
-                    Ps[(RT * ty + i) * PLD + tx + 16 * j] = p;
+                    Ps[(r0 + i) * PLD + key0 + tx + 16 * j] = p;
                 }
 #pragma unroll
                 for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
@@ -355,13 +355,13 @@ __global__ void __launch_bounds__(A_THREADS, HD <= 64 ? 2 : 1)
                     for (int e = 0; e < VW / 2; ++e) o[i][d][e] = mul_pair(o[i][d][e], cc);
             }
             __syncwarp();                  // a row's P is written and read by one half-warp
-            const int keys = min(AK, kend - c * AK);
+            const int keys = min(key0 + 16 * NJ, kend - c * AK);
 #pragma unroll 2
-            for (int j0 = 0; j0 < keys; j0 += 4) {       // (P and V behind the last key are zeros)
+            for (int j0 = key0; j0 < keys; j0 += 4) {       // (P and V behind the last key are zeros)
                 uint64_t pe[RT][4];
 #pragma unroll
                 for (int i = 0; i < RT; ++i) {
-                    const float4 t = *reinterpret_cast<const float4*>(Ps + (RT * ty + i) * PLD + j0);
+                    const float4 t = *reinterpret_cast<const float4*>(Ps + (r0 + i) * PLD + j0);
                     pe[i][0] = pair_of(t.x); pe[i][1] = pair_of(t.y);
                     pe[i][2] = pair_of(t.z); pe[i][3] = pair_of(t.w);
                 }
@@ -384,15 +384,69 @@ __global__ void __launch_bounds__(A_THREADS, HD <= 64 ? 2 : 1)
                     }
             }
             __syncwarp();
+        };
+
+        for (int c = first; c < chunks; ++c) {
+            if (STAGES == 1) {
+                __syncthreads();
+                load(c);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncthreads();               // chunk c is there; chunk c - 1 has been read
+            if (STAGES > 1 && c + 1 < chunks) load(c + 1);
+            if (!warp_live) continue;
+            if (groups == 1) attend(c, std::integral_constant<int, 4>());
+            else if (groups == 2) attend(c, std::integral_constant<int, 2>());
+            else attend(c, std::integral_constant<int, 1>());
         }
         __syncthreads();                   // bad_s is final
         const bool bad = k.q.bad || bad_s;
+        if (groups > 1) {                  // the groups' partial results into the first one's
+            float* os = KVs;               // [groups - 1][span][LD], then their m and l
+            float* ms = os + (size_t)(AQ - span) * LD;
+            if (kg > 0 && warp_live) {
+#pragma unroll
+                for (int i = 0; i < RT; ++i) {
+                    const int at = (kg - 1) * span + r0 + i;
+#pragma unroll
+                    for (int d = 0; d < NV; ++d)
+#pragma unroll
+                        for (int e = 0; e < VW / 2; ++e)
+                            *reinterpret_cast<uint64_t*>(os + at * LD + tx * VW + 16 * VW * d + 2 * e) = o[i][d][e];
+                    if (tx == 0) {
+                        ms[at] = m[i];
+                        ms[AQ + at] = l[i];
+                    }
+                }
+            }
+            __syncthreads();
+            if (kg == 0 && warp_live) {
+                for (int x = 0; x < groups - 1; ++x)
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) {
+                        const int at = x * span + r0 + i;
+                        const float mn = fmaxf(m[i], ms[at]), f = ex2(m[i] - mn), f2 = ex2(ms[at] - mn);
+                        m[i] = mn;
+                        l[i] = fmaf(l[i], f, ms[AQ + at] * f2);
+                        const uint64_t ff = pair_of(f), ff2 = pair_of(f2);
+#pragma unroll
+                        for (int d = 0; d < NV; ++d)
+#pragma unroll
+                            for (int e = 0; e < VW / 2; ++e) {
+                                uint64_t t = mul_pair(o[i][d][e], ff);
+                                fma_pair(t, ff2, *reinterpret_cast<const uint64_t*>(os + at * LD + tx * VW +
+                                                                                    16 * VW * d + 2 * e));
+                                o[i][d][e] = t;
+                            }
+                    }
+            }
+        }
         const bool whole = first == 0 && chunks == k.units;
         float* p = part + (size_t)(2 * w + (first == 0 ? 1 : 0)) * part_floats(HD);
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
-            const int q = RT * ty + i;
-            if (q >= rows) continue;
+            const int q = r0 + i;
+            if (kg > 0 || q >= rows) continue;
             if (bad) l[i] = __int_as_float(0x7fc00000);
             if (!whole && tx == 0) {
                 p[AQ * HD + q] = m[i];
