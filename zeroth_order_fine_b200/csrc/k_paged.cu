@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(KW_THREADS)
 constexpr int AQ = 64, AK = 64, A_THREADS = 256;
 constexpr int RT = 4;                      // query rows of a thread, 16 threads side by side on 64 keys
 constexpr int A_GROUPS = 1024;             // prefix entries, in the chunk buffers before their use
-using Line = PagedLine<false, AQ, AK>;
+using Line = PagedLine<false, AQ, AK, 3>;
 
 // Floats of a partial result: o [AQ][hd], m [AQ], l [AQ].
 __host__ __device__ constexpr int part_floats(int hd) { return AQ * (hd + 2); }
@@ -206,12 +206,14 @@ __global__ void __launch_bounds__(A_THREADS, HD <= 64 ? 2 : 1)
     long long* cum = reinterpret_cast<long long*>(KVs);
     const long long L = Line::prefix(a, A_GROUPS, cum, cum + A_GROUPS + 1);
     const int w = blockIdx.x;
-    const long long stretch = div_ll(L + gridDim.x - 1, gridDim.x);
+    const long long stretch = max(div_ll(L + gridDim.x - 1, gridDim.x), (long long)Line::WMAX);
     const long long u1 = min(L, stretch * (w + 1));
     long long u = stretch * w;
     if (tid == 0) desc[w].pieces = 0;
     if (u >= u1) return;
     Line::Cursor k = Line::locate(a, A_GROUPS, cum, u);
+    if (u >= u1) return;                   // no unit begins here
+    if (k.unit == k.units) Line::advance(a, k, 0, true);
 
     const float sl2 = a.scale * 1.4426950408889634f;      // scores in units of ln 2
     const int n_pages = (int)(a.n_slots >> a.page_shift);
@@ -222,7 +224,8 @@ __global__ void __launch_bounds__(A_THREADS, HD <= 64 ? 2 : 1)
     constexpr int VW = HD >= 64 ? 4 : 2, NV = HD / (16 * VW);
     while (u < u1) {
         const int row0 = k.tile * AQ, rows = min(AQ, k.q.rows - row0), kvh = k.head;
-        const int first = k.unit, chunks = (int)min((long long)k.units, k.unit + (u1 - u));
+        const int wt = Line::weight(k.q, k.tile);
+        const int first = k.unit, chunks = (int)min((long long)k.units, k.unit + div_ll(u1 - u + wt - 1, wt));
         const int kend = Line::keys(a, k.q, row0 + AQ);
         const int* table = a.block_table + (size_t)k.r * a.max_blocks;
         __syncthreads();                   // what the piece before (or the search) read is free
@@ -467,14 +470,14 @@ __global__ void __launch_bounds__(A_THREADS, HD <= 64 ? 2 : 1)
         }
         if (!whole && first == 0 && tid == 0) {
             PagedDesc d;
-            d.pieces = (int)((u + k.units - 1) / stretch) - w + 1;
+            d.pieces = (int)div_ll(u + (long long)(k.units - 1) * wt, stretch) - w + 1;
             d.start = k.q.start;
             d.row0 = row0;
             d.rows = rows;
             d.kvh = kvh;
             desc[w] = d;
         }
-        u += chunks - first;
+        u += (long long)(chunks - first) * wt;
         Line::advance(a, k, chunks - first, u < u1);
     }
 }

@@ -338,7 +338,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const long long L = Line::prefix(a, GROUPS, cum, wsum);
     const int w = blockIdx.x;
     const long long stretch = div_ll(L + gridDim.x - 1, gridDim.x);
-    const long long u0 = stretch * w, u1 = min(L, u0 + stretch);
+    long long u0 = stretch * w;
+    const long long u1 = min(L, u0 + stretch);
     if (tid == 0) desc[w].pieces = 0;
     if (u0 >= u1) return;                             // the whole CTA
     if (warp == 0) {

@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int workers = gridDim.x * (WARPS / team), w = blockIdx.x * (WARPS / team) + warp / team;
     const int mate = warp % team;                     // the warp's head within the team's
     const long long stretch = div_ll(L + workers - 1, workers);      // units per worker
-    const long long u0 = stretch * w, u1 = min(L, u0 + stretch);
+    long long u0 = stretch * w;
+    const long long u1 = min(L, u0 + stretch);
     if (mate == 0 && lane == 0) desc[w].pieces = 0;
     if (u0 >= u1) return;                             // nothing to do, nothing in flight
 

@@ -23,8 +23,12 @@ __device__ __forceinline__ int mod_g(const PagedArgs& a, int x) { return x - by_
 // A kernel takes the requests of at most step_tokens new tokens (BIG false) or the others (BIG
 // true); the rest have no rows for it.  RB query rows (new tokens x g of one kv head) make a tile,
 // UK keys a unit; a place on the line stands for line_heads-th parts of the kv heads.
-template <bool BIG, int RB, int UK>
+// W0 > 0: a unit of a tile of n rows is W0 + ceil(n / 8) steps of the line and not one, where a unit
+// of few rows takes less time; a stretch has the units that begin in it and is at least WMAX long,
+// so that every stretch inside an item has some of its units.
+template <bool BIG, int RB, int UK, int W0 = 0>
 struct PagedLine {
+    static constexpr int WMAX = W0 ? W0 + RB / 8 : 1;
     struct Req {
         int start, rows, ctx;             // first packed row, rows per kv head, tokens before
         bool bad;                         // the length cannot be used: NaN rows
@@ -53,10 +57,13 @@ struct PagedLine {
     static __device__ __forceinline__ int units(const PagedArgs& a, const Req& q, int t) {
         return q.bad ? 1 : (keys(a, q, (t + 1) * RB) + UK - 1) / UK;
     }
+    static __device__ __forceinline__ int weight(const Req& q, int t) {       // steps of a unit of tile t
+        return W0 ? W0 + (min(RB, q.rows - t * RB) + 7) / 8 : 1;
+    }
     static __device__ __forceinline__ long long req_units(const PagedArgs& a, int r) {
         const Req q = get(a, r);
         long long u = 0;
-        for (int t = 0; t * RB < q.rows; ++t) u += units(a, q, t);
+        for (int t = 0; t * RB < q.rows; ++t) u += (long long)units(a, q, t) * weight(q, t);
         return u * a.line_heads;
     }
     // Prefix sums of the requests' units in groups of ceil(n_rows / max_groups) requests: cum[0 ..
@@ -93,9 +100,11 @@ struct PagedLine {
         __syncthreads();
         return base;
     }
-    // The place of unit u (below the total); a whole warp calls it with the same u, max_groups <= 1024.
+    // The place of the first unit that begins at step u (below the total) or behind it, u then moved
+    // there; with W0 it may be unit = units, the end of an item.  A whole warp calls it with the same
+    // u, max_groups <= 1024.
     static __device__ __forceinline__ Cursor locate(const PagedArgs& a, int max_groups,
-                                                    const long long* cum, long long u) {
+                                                    const long long* cum, long long& u) {
         const int c = (a.n_rows + max_groups - 1) / max_groups;
         const int groups = c == 1 ? a.n_rows : (a.n_rows + c - 1) / c, lane = threadIdx.x & 31;
         int lo = 0;                                    // the last group with cum <= u
@@ -116,15 +125,19 @@ struct PagedLine {
             }
         k.q = get(a, k.r);
         k.tile = 0;
+        int wt;
         for (;;) {
             k.units = units(a, k.q, k.tile);
-            const long long n = (long long)k.units * a.line_heads;
+            wt = weight(k.q, k.tile);
+            const long long n = (long long)k.units * wt * a.line_heads;
             if (rest < n) break;
             rest -= n;
             ++k.tile;
         }
-        k.head = (int)div_ll(rest, k.units);
-        k.unit = (int)(rest - (long long)k.head * k.units);
+        k.head = (int)div_ll(rest, (long long)k.units * wt);
+        rest -= (long long)k.head * k.units * wt;
+        k.unit = W0 ? (int)div_ll(rest + wt - 1, wt) : (int)rest;
+        u += (long long)k.unit * wt - rest;
         return k;
     }
     // On by n units of the same (request, tile, head), n <= units - unit; `more`: the line goes on
