@@ -201,7 +201,9 @@ __global__ void __launch_bounds__(A_THREADS, HD <= 64 ? 2 : 1)
     float* Ps = Qs + AQ * LD;              // [AQ][PLD]
     float* KVs = Ps + AQ * PLD;            // [STAGES][2][AK][LD]
     __shared__ int bad_s;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    // 16 threads of the same parity in a warp share their rows: neighbouring lanes then read the same
+    // keys and values, and a 16-byte read of a warp takes half the passes
+    const int tid = threadIdx.x, tx = (tid >> 1) & 15, ty = 2 * (tid >> 5) + (tid & 1);
     grid_dep_launch();
     long long* cum = reinterpret_cast<long long*>(KVs);
     const long long L = Line::prefix(a, A_GROUPS, cum, cum + A_GROUPS + 1);
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(A_THREADS, HD <= 64 ? 2 : 1)
                     if (see[j]) mx = fmaxf(mx, s[i][j]);
                 }
 #pragma unroll
-                for (int x = 8; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+                for (int x = 16; x > 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
                 const float mn = fmaxf(m[i], mx);
                 const float corr = ex2(m[i] - mn);
                 float sum = 0.f;
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(A_THREADS, HD <= 64 ? 2 : 1)
                     Ps[(r0 + i) * PLD + key0 + tx + 16 * j] = p;
                 }
 #pragma unroll
-                for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                for (int x = 16; x > 1; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
                 l[i] = l[i] * corr + sum;
                 m[i] = mn;
                 const uint64_t cc = pair_of(corr);
@@ -357,7 +359,7 @@ __global__ void __launch_bounds__(A_THREADS, HD <= 64 ? 2 : 1)
 #pragma unroll
                     for (int e = 0; e < VW / 2; ++e) o[i][d][e] = mul_pair(o[i][d][e], cc);
             }
-            __syncwarp();                  // a row's P is written and read by one half-warp
+            __syncwarp();                  // a row's P is written and read by one warp
             const int keys = min(key0 + 16 * NJ, kend - c * AK);
 #pragma unroll 2
             for (int j0 = key0; j0 < keys; j0 += 4) {       // (P and V behind the last key are zeros)
