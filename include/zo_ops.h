@@ -246,7 +246,7 @@ int zo_op_block_tables(const int32_t* old_lens, const int32_t* new_lens, int32_t
  *   qkv       dev [n_tokens x ld_qkv] dtype, q | k | v per row as for zo_op_attention
  *   slot_map  dev int32 [n_tokens]; rows whose slot is outside [0, n_slots) are not written
  *   cache     dev [n_slots x 2 * n_kv_heads * head_dim] dtype
- * When two rows name the same slot, which of them it ends up holding is not defined.
+ * When two rows name the same slot, it ends up with parts of either.
  * ZO_ERR_ARG on NULL pointers, negative sizes, or ld_qkv < (n_heads + 2 n_kv_heads) *
  * head_dim. */
 int zo_op_kv_write(const void* qkv, int64_t ld_qkv, const int32_t* slot_map, int32_t n_tokens,
@@ -275,14 +275,15 @@ int zo_op_kv_write(const void* qkv, int64_t ld_qkv, const int32_t* slot_map, int
  *   impl     ZO_IMPL_TENSOR_CORES needs bf16, head_dim 64 or 128, at most 128 query heads per
  *            kv head, 16-byte aligned pointers and strides that are multiples of 8 elements;
  *            AUTO picks it then, else CUDA cores
- * A request whose lens is below its new tokens or above max_blocks * page_size, or that names
- * a page outside [0, n_slots / page_size) within its length, gets NaN rows; one whose rows are
+ * A request whose lens is below its new tokens or above max_blocks * page_size or 2^31 - 256, or
+ * that names a page outside [0, n_slots / page_size) within its length, gets NaN rows; one whose rows are
  * not inside [0, n_tokens) is left out.  A non-finite key or value can make every row of its
  * own request NaN, also rows before it.
  * ZO_ERR_ARG on NULL pointers, sizes below 1 (n_rows, n_tokens: below 0), n_heads not a
  * multiple of n_kv_heads, strides below the row, a page_size that is no power of two from 8
  * to 256, n_slots no multiple of page_size or above 2^31 - 1, or a workspace too small;
- * ZO_ERR_UNSUPPORTED for head_dim other than 32, 64, 128, 256. */
+ * ZO_ERR_UNSUPPORTED for head_dim other than 32, 64, 128, 256, more than 65535 kv heads, or
+ * n_tokens * n_heads / n_kv_heads above 2^30. */
 size_t zo_op_attention_paged_workspace(int32_t n_tokens, int32_t n_rows, int32_t n_heads,
                                        int32_t n_kv_heads, int32_t head_dim, int32_t dtype);
 int zo_op_attention_paged(const void* q, int64_t ld_q, const void* cache, int64_t n_slots,
@@ -307,7 +308,8 @@ int zo_op_attention_paged(const void* q, int64_t ld_q, const void* cache, int64_
  *   impl ZO_IMPL_TENSOR_CORES needs dtype bf16, K, N and n_adapters * rank multiples of 8 and
  *        16-byte aligned pointers; AUTO picks it then, else CUDA cores
  * M = 0 is a no-op.  ZO_ERR_ARG on NULL pointers, negative or empty sizes, rank above 256 or
- * n_adapters * rank above 65536, an unknown act, or a workspace too small or not aligned. */
+ * n_adapters * rank above 65536, an unknown act, or a workspace too small or not aligned;
+ * ZO_ERR_UNSUPPORTED for M above 4194240. */
 size_t zo_op_linear_adapters_workspace(int32_t M, int32_t N, int32_t K, int32_t n_adapters,
                                        int32_t rank, int32_t dtype);
 int zo_op_linear_adapters(const void* x, const void* W, const float* bias, const void* A,

@@ -540,6 +540,150 @@ def test_linear_adapters_in_a_graph_follow_the_ids(M):
     assert zo.zo_op_error_word() == 0
 
 
+def test_attention_paged_length_at_the_end_of_int():
+    """A length whose last unit of keys would not fit an int: NaN rows, the other request as ever."""
+    from zeroth_order_fine_b200 import zo
+    for dt, impl in ((BF, 0), (BF, 1), (FP, 1)):
+        for new in (1, 40):
+            c = Paged([(0, new), (300, new)], 4, 2, 128, 256, dt)
+            table = torch.zeros(2, 2 ** 31 // 256, dtype=torch.int32, device="cuda")
+            table[:, :c.blocks] = i32(c.table)
+            out = zo.zo_op_attention_paged(c.q.cuda(), c.cache.cuda(), table, 256, i32(c.cu),
+                                           i32([2 ** 31 - 1, 300 + new]), new, 4, 2, 128, impl=impl)
+            assert torch.isnan(out[:new]).all()
+            c.check(out, impl, skip=(0,))
+    assert zo.zo_op_error_word() == 0
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_attention_paged_and_write_far_into_a_cache(new):
+    """Pages past 2^32 bytes and 2^32 elements of the cache: the same rows as from a small one."""
+    from zeroth_order_fine_b200 import zo
+    Hq, Hkv, hd, p = 8, 8, 128, 16
+    rows = 2 ** 21 + 64 * p                           # 4 KB each in bf16, 2^32 elements at 2^21 rows
+    big = torch.empty(rows, 2 * Hkv * hd, dtype=BF, device="cuda")
+    pages = torch.arange(rows // p - 8, rows // p).flip(0)
+    g = torch.Generator().manual_seed(new)
+    lens, T = [50, 61], 2 * new
+    qkv = torch.randn(sum(lens), (Hq + 2 * Hkv) * hd, generator=g).to(BF).cuda()
+    q = qkv[:T]
+    for impl in (0, 1):
+        outs = []
+        for cache, first in ((big, pages[:8].tolist()), (torch.empty(8 * p, 2 * Hkv * hd, dtype=BF,
+                                                                     device="cuda"), list(range(8)))):
+            table = [first[:4], first[4:]]
+            slots = sum([[table[r][i // p] * p + i % p for i in range(n)] for r, n in enumerate(lens)], [])
+            zo.zo_op_kv_write(qkv, i32(slots), cache, Hq, Hkv, hd)
+            outs.append(zo.zo_op_attention_paged(q, cache, i32(table), p, i32([0, new, T]), i32(lens), new,
+                                                 Hq, Hkv, hd, impl=impl))
+        assert torch.equal(*outs) and torch.isfinite(outs[0]).all()
+
+
+@pytest.mark.parametrize("M", [5, 40, 300, 2500])
+def test_linear_adapters_of_65536_factor_columns(M):
+    """The most adapters there can be; 2500 rows: two passes of the tiles form."""
+    from zeroth_order_fine_b200 import zo
+    n, r, N, K = 4096, 16, 64, 64
+    ids = [0, n - 1] + spans(M - 2, n, M, 1, 60)
+    x, W, A, B, idt, sc, b = adapt_case(M, N, K, n, r, ids, BF, seed=M)
+    y = zo.zo_op_linear_adapters(x.cuda(), W.cuda(), A.cuda(), B.cuda(), idt.cuda(), sc.cuda(), b.cuda())
+    ref, tol = adapt_ref(x, W, A, B, idt, sc, b, n, r, True, True)
+    assert torch.all((y.double().cpu() - ref).abs() <= tol)
+    assert zo.zo_op_error_word() == 0
+
+
+def test_linear_adapters_output_past_32_bits():
+    from zeroth_order_fine_b200 import zo
+    M, N, K, n, r = 270000, 8192, 64, 8, 16           # 2^31 elements at row 262144
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn(64, K, generator=g).to(BF)
+    _, W, A, B, _, sc, b = adapt_case(1, N, K, n, r, [0], BF)
+    xs = x.repeat(-(-M // 64), 1)[:M].cuda()
+    ids = [(i * 7) % 9 - 1 for i in range(64)]
+    idt = i32(ids).repeat(-(-M // 64))[:M]
+    y = zo.zo_op_linear_adapters(xs, W.cuda(), A.cuda(), B.cuda(), idt, sc.cuda(), b.cuda())
+    ref, tol = adapt_ref(x, W, A, B, i32(ids, "cpu"), sc, b, n, r, True, True)
+    for m in (0, 262080, 262144, 262208, 269952 - 64):  # blocks of 64 rows, on both sides of the pass
+        assert torch.all((y[m:m + 64].double().cpu() - ref).abs() <= tol), m
+    assert zo.zo_op_error_word() == 0
+
+
+# ---- two at once --------------------------------------------------------------------------------
+
+def shared_calls():
+    """Calls of every kernel, each with its own output and workspace; the result of each alone."""
+    from zeroth_order_fine_b200 import zo
+    calls = []
+    for dt, reqs in ((BF, [(700, 1), (33, 1), (2000, 1)]), (BF, [(500, 200), (40, 1), (0, 130)]),
+                     (FP, [(300, 1), (20, 70), (900, 3)])):
+        c = Paged(reqs, 8, 2, 128, 16, dt, seed=len(calls), tail=0)
+        q, args = c.q.cuda(), c.args()
+        out = torch.zeros(c.T, 8 * 128, dtype=dt, device="cuda")
+        ws = torch.empty(zo.zo_op_attention_paged_workspace(c.T, len(reqs), 8, 2, 128, dt),
+                         dtype=torch.uint8, device="cuda")
+        calls.append((out, lambda q=q, a=args, m=c.max_new, o=out, w=ws: zo.zo_op_attention_paged(
+            q, *a, m, 8, 2, 128, out=o, ws=w)))
+    for M, N, K, dt in ((1, 1024, 512, BF), (70, 1024, 512, BF), (700, 1024, 512, BF), (90, 512, 256, FP)):
+        x, W, A, B, ids, sc, b = (t.cuda() for t in adapt_case(M, N, K, 6, 16, spans(M, 6, M), dt))
+        out = torch.zeros(M, N, dtype=dt, device="cuda")
+        ws = torch.empty(zo.zo_op_linear_adapters_workspace(M, N, K, 6, 16, dt), dtype=torch.uint8,
+                         device="cuda")
+        calls.append((out, lambda x=x, W=W, A=A, B=B, i=ids, s=sc, b=b, o=out, w=ws:
+                      zo.zo_op_linear_adapters(x, W, A, B, i, s, b, out=o, ws=w)))
+    want = []
+    for out, call in calls:
+        call()
+        torch.cuda.synchronize()
+        want.append(out.clone())
+    return calls, want
+
+
+def test_serving_calls_on_two_streams_at_once():
+    from zeroth_order_fine_b200 import zo
+    (one, want), (two, _) = shared_calls(), shared_calls()
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for shift in range(len(one)):
+        for out, _ in one + two:
+            out.zero_()
+        torch.cuda.synchronize()
+        for i in range(len(one)):                     # every call beside every other
+            with torch.cuda.stream(s[0]):
+                one[i][1]()
+            with torch.cuda.stream(s[1]):
+                two[(i + shift) % len(two)][1]()
+        torch.cuda.synchronize()
+        for set_ in (one, two):
+            for i, (out, _) in enumerate(set_):
+                assert torch.equal(out, want[i]), (shift, i)
+    assert zo.zo_op_error_word() == 0
+
+
+def test_serving_calls_in_two_graphs_at_once():
+    from zeroth_order_fine_b200 import zo
+    sets = [shared_calls(), shared_calls()]
+    graphs, s = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for k, (calls, _) in enumerate(sets):
+        order = calls if k == 0 else calls[::-1]
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            for _, call in order:
+                call()
+        graphs.append(gr)
+    for _ in range(5):
+        for calls, _ in sets:
+            for out, _ in calls:
+                out.zero_()
+        torch.cuda.synchronize()
+        for gr, st in zip(graphs, s):
+            with torch.cuda.stream(st):
+                gr.replay()
+        torch.cuda.synchronize()
+        for calls, want in sets:
+            for i, (out, _) in enumerate(calls):
+                assert torch.equal(out, want[i]), i
+    assert zo.zo_op_error_word() == 0
+
+
 # ---- together ---------------------------------------------------------------------------------
 
 def test_serving_run_over_pages_equals_the_packed_attention():

@@ -115,9 +115,9 @@ __global__ void __launch_bounds__(256) adapter_gemm_kernel(AdapterArgs a, const 
 // tiles, 8 x 4 outputs a thread, K in 32-deep stages by asynchronous 16-byte copies.  The tiles stay
 // as they lie in memory (K contiguous, rows padded to 36 floats): a thread reads 4 of K at a time of
 // its 8 rows and 4 columns, 12 16-byte reads for 128 FMAs, without bank clashes, two FMAs to an
-// instruction (neighbouring k).  K is also split
-// over CTAs where the tiles alone would leave the last round of SMs half empty; each split writes a
-// slice, and the slices are added in order by the kernel that adds the expand.
+// instruction (neighbouring k).  K is also split over CTAs where the tiles alone would leave the
+// last round of SMs half empty; each split writes a slice, and the slices are added in order by the
+// kernel that adds the expand.
 constexpr int FM = 64, FK = 32, FLD = FK + 4, FSTAGES = 3, F_THREADS = 128;
 constexpr int F_SMEM = FSTAGES * 2 * FM * FLD * 4;
 
@@ -412,7 +412,6 @@ __global__ void __launch_bounds__(128)
 __global__ void __launch_bounds__(256)
     adapter_lists_kernel(const int* __restrict__ ids, int M, int n_adapters, int rank, int* __restrict__ cnt,
                          int* __restrict__ list, int n_list) {
-    // (blocks past the last one have no steps)
     __shared__ unsigned steps[4096 / 32];       // one bit per 16-column step of 65536 columns
     __shared__ int wsum[8];
     grid_dep_launch();

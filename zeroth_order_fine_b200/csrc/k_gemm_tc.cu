@@ -1092,9 +1092,10 @@ __device__ __forceinline__ int tile_row(int t, const TcParams& p) {
 }
 
 // A row block's list of extension blocks, its first entries in registers: the producer and the issuer
-// each load the next tile's while they work on this one, since a load where an entry is needed
-// stalled them for an L2 round trip each (4093 rows, OPT-13B FFN input, ~4 blocks a tile: 930 us
-// instead of 744).
+// each load the next tile's behind this one's main loop, so that no load stands where an entry is
+// needed.  The listed blocks have loops of their own in both: with the list's tests inside the main
+// loops the single issuing thread fell behind the tensor cores (4093 rows, OPT-13B FFN input, ~4
+// blocks a tile: 848 us instead of 729).
 struct BlockList {
     static constexpr int N = 8;              // entries kept; lists are padded to a multiple of them
     int mb, cnt, e[N];

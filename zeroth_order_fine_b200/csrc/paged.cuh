@@ -46,7 +46,8 @@ struct PagedLine {
         const bool in = s >= 0 && e >= s && e <= a.n_tokens;
         q.start = s;
         q.rows = in && (n > a.step_tokens) == BIG ? n * a.g : 0;
-        q.bad = len < n || (long long)len > ((long long)a.max_blocks << a.page_shift);
+        // (the last 256 lengths of an int: a unit's end would not fit)
+        q.bad = len < n || len > 0x7fffff00 || (long long)len > ((long long)a.max_blocks << a.page_shift);
         q.ctx = len - n;
         return q;
     }
