@@ -131,7 +131,8 @@ __global__ void __launch_bounds__(F_THREADS)
                     float* __restrict__ slices) {
     extern __shared__ __align__(16) float fsm[];
     grid_dep_launch();
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    // neighbouring lanes read the same columns: a 16-byte read of a warp takes half the passes
+    const int tid = threadIdx.x, tx = (tid >> 1) & 15, ty = 2 * (tid >> 5) + (tid & 1);
     const int m0 = blockIdx.y * FM, n0 = blockIdx.x * FM, split = blockIdx.z;
     const int blocks = (K + FK - 1) / FK, per = (blocks + ks - 1) / ks;
     const int b0 = split * per, b1 = min(blocks, b0 + per);
