@@ -137,15 +137,19 @@ __global__ void __launch_bounds__(F_THREADS)
     const int blocks = (K + FK - 1) / FK, per = (blocks + ks - 1) / ks;
     const int b0 = split * per, b1 = min(blocks, b0 + per);
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(fsm));
+    // 8 copies a thread and stage: 4 of each operand's 16-row steps, 4 columns of K
+    const int lr = tid / (FK / 4), lc = tid % (FK / 4) * 4;
+    const float *pa = A + (size_t)(m0 + lr) * K + lc, *pb = B + (size_t)(n0 + lr) * K + lc;
+    const uint32_t to = base + (uint32_t)(lr * FLD + lc) * 4;
     auto load = [&](int b) {
-        const uint32_t st = base + (uint32_t)((b - b0) % FSTAGES) * (2 * FM * FLD * 4);
+        const uint32_t st = to + (uint32_t)((b - b0) % FSTAGES) * (2 * FM * FLD * 4);
+        const int k = b * FK;
 #pragma unroll
-        for (int i = tid; i < 2 * FM * FK / 4; i += F_THREADS) {
-            const int op = i / (FM * FK / 4), r = i / (FK / 4) % FM, c = i % (FK / 4) * 4, k = b * FK + c;
-            const int row = (op ? n0 : m0) + r, rows = op ? N : M;
-            const bool live = row < rows && k < K;
-            const float* src = (op ? B : A) + (live ? (size_t)row * K + k : 0);
-            cp16(st + (uint32_t)((op * FM + r) * FLD + c) * 4, src, live);
+        for (int i = 0; i < 2 * FM / 16; ++i) {
+            const int r = i % (FM / 16) * 16;
+            const bool live = (i < FM / 16 ? m0 : n0) + lr + r < (i < FM / 16 ? M : N) && k + lc < K;
+            const float* src = (i < FM / 16 ? pa : pb) + (live ? (size_t)r * K + k : 0);
+            cp16(st + (uint32_t)(i * 16 * FLD) * 4, live ? src : A, live);
         }
     };
     uint64_t acc[8][4];                        // sums over the even and over the odd k
