@@ -373,9 +373,10 @@ int zo_op_attention_paged(const void* q, int64_t ld_q, const void* cache, int64_
     a.ws = ws;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (impl != ZO_IMPL_CUDA_CORES && paged_tc_supported(a)) {
-        // up to 16 query rows per kv head: the decode-step kernel; more: the chunk kernel
+        // Requests of up to 16 query rows per kv head: the decode-step kernel; others: the chunk
+        // kernel.  A request alone is the one that max_new speaks of (and the chunk kernel takes any).
         const bool chunks = (int64_t)max_new * a.g > 16;
-        a.step_tokens = chunks ? 16 / a.g : 0x7fffffff;
+        a.step_tokens = !chunks ? 0x7fffffff : n_rows == 1 ? 0 : 16 / a.g;
         if (a.step_tokens > 0 && launch_paged_step(a, st) != cudaSuccess)
             return op_fail("paged attention launch failed");
         if (chunks && launch_paged_chunk(a, st) != cudaSuccess)
