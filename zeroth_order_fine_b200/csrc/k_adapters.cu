@@ -111,7 +111,9 @@ __global__ void __launch_bounds__(256) adapter_gemm_kernel(AdapterArgs a, const 
 
 
 // ---- fp32 -----------------------------------------------------------------------------------
-// The product in fp32 on CUDA cores, bound by their FMA rate (2 M N K flops at ~70 TFLOP/s): 64 x 64
+// The product in fp32 on CUDA cores, bound by their FMA rate (2 M N K flops at ~70 TFLOP/s; 301 x 2048 x
+// 2048 with its adapters 76 us, of which this kernel ~65: the FMA pipe is 63 % busy while an SM works
+// and the SMs work 91 % of the time; 48-byte spills at 128 registers for a fourth CTA gave nothing): 64 x 64
 // tiles, 8 x 4 outputs a thread, K in 32-deep stages by asynchronous 16-byte copies.  The tiles stay
 // as they lie in memory (K contiguous, rows padded to 36 floats): a thread reads 4 of K at a time of
 // its 8 rows and 4 columns, 12 16-byte reads for 128 FMAs, without bank clashes, two FMAs to an
@@ -251,7 +253,8 @@ __global__ void __launch_bounds__(128)
     }
 }
 
-// K splits of the fp32 product: the fewest whose last round of SMs is full enough (each costs a slice)
+// K splits of the fp32 product: the fewest whose last round of SMs is full enough (each costs a slice):
+// 301 x 2048 x 2048 under 5 adapters takes 133 us unsplit, 103 in 2, 88 in 4 and 84 in 8.
 int f32_splits(int M, int N, int K) {
     const long long tiles = (long long)((M + FM - 1) / FM) * ((N + FM - 1) / FM);
     const int blocks = (K + FK - 1) / FK;
@@ -272,19 +275,22 @@ int f32_splits(int M, int N, int K) {
 // ---- tensor-core forms ----------------------------------------------------------------------
 
 // The rows' shrink for the decode form: S[m, j] = scale[a] x[m] . A_a[j] in fp32, rounded to bf16
-// into row m of the masked S (the products' extension operand), whose other columns become zeros in
-// the blocks that any row uses.  KW warps share a dot, each with its part of K (few rows: the chain of
-// loads is what takes time), or a warp takes JW of the adapter's rows, so that x[m] is read once for
-// them (many); 16-byte loads; the warps of a CTA share row m through L1.  The first CTA also writes the list
-// of blocks: those that the rows' adapters touch, with the mask of their 16-column steps.
-template <int JW, int KW>
+// into row m of the masked S (the products' extension operand, which the tensor cores take in bf16:
+// half a step of S, as the plain form in bf16 has), whose other columns become zeros in the blocks
+// that any row uses.  KW warps share a dot, each with its part of K: a whole CTA per dot while the
+// CTAs are about two a SM, since the chain of loads is what takes time (16 rows of rank 16, K = 5120,
+// the whole call: 16.9 us against 18.0), a warp per dot above (48 rows: 18.5 us against 19.1; 128 rows
+// of rank 64: 35.8 against 45.4).  16-byte loads; the warps of a CTA share row m through L1.  The
+// first CTA also writes the list of blocks: those that the rows' adapters touch, with the mask of
+// their 16-column steps.
+template <int KW>
 __global__ void __launch_bounds__(SH_WARPS * 32)
     adapter_shrink_rows_kernel(AdapterArgs a, __nv_bfloat16* __restrict__ S, int ldS, int* __restrict__ cnt,
                                int* __restrict__ list) {
     __shared__ unsigned steps[4096 / 32];      // one bit per 16-column step of 65536 columns
     grid_dep_launch();                         // the product reads S and the list only at its end
-    constexpr int PER_CTA = JW * SH_WARPS / KW;          // rows of the adapter per CTA
-    static_assert(KW == 1 || (KW == SH_WARPS && JW == 1), "a whole CTA per dot, or a warp");
+    constexpr int PER_CTA = SH_WARPS / KW;               // rows of the adapter per CTA
+    static_assert(KW == 1 || KW == SH_WARPS, "a whole CTA per dot, or a warp");
     __shared__ float parts[SH_WARPS];
     const int groups = (a.rank + PER_CTA - 1) / PER_CTA;
     const int m = (int)blockIdx.x / groups, grp = (int)blockIdx.x % groups;
@@ -328,51 +334,39 @@ __global__ void __launch_bounds__(SH_WARPS * 32)
         }
     }
     const int warp = (int)(threadIdx.x >> 5), kpart = warp % KW;
-    const int j0 = grp * PER_CTA + warp / KW * JW;
-    if (!live || j0 >= a.rank) return;         // (with KW > 1 the whole CTA)
+    const int j = grp * PER_CTA + warp / KW;
+    if (!live || j >= a.rank) return;          // (with KW > 1 the whole CTA)
     const uint4* x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + (size_t)m * a.K);
-    const uint4* f[JW];
-#pragma unroll
-    for (int q = 0; q < JW; ++q)
-        f[q] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.A) +
-                                              ((size_t)id * a.rank + min(j0 + q, a.rank - 1)) * a.K);
-    float s[JW][2];
-#pragma unroll
-    for (int q = 0; q < JW; ++q) s[q][0] = s[q][1] = 0.f;
+    const uint4* f = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.A) +
+                                                    ((size_t)id * a.rank + j) * a.K);
+    float s[2] = {0.f, 0.f};
 #pragma unroll 4
     for (int k = kpart * 32 + lane; k < a.K / 8; k += 32 * KW) {
-        float xv[8];
+        float xv[8], fv[8];
         bf8(__ldg(x + k), xv);
+        bf8(__ldg(f + k), fv);
 #pragma unroll
-        for (int q = 0; q < JW; ++q) {
-            float fv[8];
-            bf8(__ldg(f[q] + k), fv);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s[q][i & 1] = fmaf(xv[i], fv[i], s[q][i & 1]);
-        }
+        for (int i = 0; i < 8; ++i) s[i & 1] = fmaf(xv[i], fv[i], s[i & 1]);
     }
-#pragma unroll
-    for (int q = 0; q < JW; ++q) {
-        float v = warp_sum(s[q][0] + s[q][1]);
-        if (KW > 1) {
-            if (lane == 0) parts[warp] = v;
-            __syncthreads();
-            v = 0.f;
-            for (int w = 0; w < KW; ++w) v += parts[w];
-        }
-        if (lane == 0 && kpart == 0 && j0 + q < a.rank)
-            S[(size_t)m * ldS + (size_t)id * a.rank + j0 + q] = __float2bfloat16_rn(v * a.scale[id]);
+    float v = warp_sum(s[0] + s[1]);
+    if (KW > 1) {
+        if (lane == 0) parts[warp] = v;
+        __syncthreads();
+        v = 0.f;
+        for (int w = 0; w < KW; ++w) v += parts[w];
     }
+    if (lane == 0 && kpart == 0)
+        S[(size_t)m * ldS + (size_t)id * a.rank + j] = __float2bfloat16_rn(v * a.scale[id]);
 }
 
-template <int JW, int KW>
+template <int KW>
 cudaError_t launch_shrink_rows(const AdapterArgs& a, __nv_bfloat16* S, int ldS, int* cnt, int* list,
                                cudaStream_t st) {
     static std::atomic<uint64_t> share{0};
-    const cudaError_t e = smem_share(reinterpret_cast<const void*>(adapter_shrink_rows_kernel<JW, KW>), share);
+    const cudaError_t e = smem_share(reinterpret_cast<const void*>(adapter_shrink_rows_kernel<KW>), share);
     if (e != cudaSuccess) return e;
-    adapter_shrink_rows_kernel<JW, KW>
-        <<<a.M * cdiv(a.rank, JW * SH_WARPS / KW), SH_WARPS * 32, 0, st>>>(a, S, ldS, cnt, list);
+    adapter_shrink_rows_kernel<KW>
+        <<<a.M * cdiv(a.rank, SH_WARPS / KW), SH_WARPS * 32, 0, st>>>(a, S, ldS, cnt, list);
     return cudaGetLastError();
 }
 
@@ -488,7 +482,9 @@ __global__ void __launch_bounds__(FIX_THREADS)
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-constexpr int STEP_ROWS = 128;           // rows up to which the decode form is taken
+// Rows up to which the decode form is taken, the most it can (OPT-13B FFN input under 32 adapters of
+// rank 16: 64 rows 63 us, the tiles form 99; 128 rows 68 and 101).
+constexpr int STEP_ROWS = 128;
 
 // Slices of the decode form: room for up to 16 splits, 64 MB at most unless one slice is more.
 size_t slice_floats(int M, int N) {
@@ -603,11 +599,8 @@ cudaError_t launch_linear_adapters_tc(const AdapterArgs& a, cudaStream_t st) {
         g.adapt_tiles = &at;
         if (!gemm_tc_supported(g)) return cudaErrorNotSupported;
         __nv_bfloat16* S = static_cast<__nv_bfloat16*>(at.S);
-        // dots: under one CTA per SM a CTA each; once warps fill the SMs, four per warp
-        const int dots = a.M * a.rank;
-        const cudaError_t e = dots <= 148                  ? launch_shrink_rows<1, SH_WARPS>(a, S, t.ld, cnt, list, st)
-                              : dots >= 4 * 148 * SH_WARPS ? launch_shrink_rows<4, 1>(a, S, t.ld, cnt, list, st)
-                                                           : launch_shrink_rows<1, 1>(a, S, t.ld, cnt, list, st);
+        const cudaError_t e = a.M * a.rank <= 2 * 148 ? launch_shrink_rows<SH_WARPS>(a, S, t.ld, cnt, list, st)
+                                                      : launch_shrink_rows<1>(a, S, t.ld, cnt, list, st);
         if (e != cudaSuccess) return e;
         return gemm_tc(g, st) ? cudaErrorUnknown : cudaSuccess;
     }

@@ -24,6 +24,13 @@
 // steps that hold keys, and the rest of the last step is cleared in shared memory.
 // Every wait is bounded; on expiry the kernel records the error word, lets what it issued land,
 // frees its tensor memory and returns.
+//
+// Measured: 1024 tokens over 16111 cached, 32 query and 8 kv heads of 128 (279 GFLOP): 254 us, 1.10
+// PFLOP/s, 0.67 of the measured burst peak; back to back under the power cap 298 us.  The chain of a
+// unit (S ready, exponentials, P stored, P V, the next Q K of the tile) bounds it: per tile and unit
+// the softmax warps work ~1150 of ~1450 cycles and wait for S the rest.  Slower: two issuing warps, one
+// a tile (343 us); 64-key halves with S twice in TMEM (304); both softmax groups on one tile with an
+// exchange of maxima (292); all exponentials on the MUFU pipe (282).
 #include <float.h>
 
 #include <type_traits>

@@ -24,6 +24,13 @@
 //   the packed attention does (the sum l is of the unrounded values).
 // Keys a query may not see get probability exactly 0; value rows behind the tile's last key are
 // cleared in registers (0 x NaN would not be 0).
+//
+// Measured: 61 requests of 300-4000 tokens, 32 query and 8 kv heads of 128: 100 us, 5.5 TB/s of the
+// cache, 0.85 of the measured HBM rate, of which the join takes 5.  32 requests of 15-160 tokens, 40
+// heads: 24.4 us for 60 MB.  The kernel's 13 us of those are 2.5 us before the first copy (lengths,
+// prefix sums, the table), 8.5 us at 6.9 TB/s and a tail where CTAs change requests; launch and join
+// take the rest.  A team per head instead of per 8 (team = 1): 25.1 and 101.2 us against 24.4 and
+// 100.8, as cache rows then come in pieces.
 #include <float.h>
 
 #include "paged.cuh"
