@@ -26,11 +26,14 @@
 // frees its tensor memory and returns.
 //
 // Measured: 1024 tokens over 16111 cached, 32 query and 8 kv heads of 128 (279 GFLOP): 254 us, 1.10
-// PFLOP/s, 0.67 of the measured burst peak; back to back under the power cap 298 us.  The chain of a
-// unit (S ready, exponentials, P stored, P V, the next Q K of the tile) bounds it: per tile and unit
-// the softmax warps work ~1150 of ~1450 cycles and wait for S the rest.  Slower: two issuing warps, one
-// a tile (343 us); 64-key halves with S twice in TMEM (304); both softmax groups on one tile with an
-// exchange of maxima (292); all exponentials on the MUFU pipe (282).
+// PFLOP/s, 0.67 of the measured burst peak; back to back under the power cap 298 us.  Of the ~3640
+// cycles of a unit (clock64 in the roles) each tile's softmax warps work 1670 and wait 1670 for S; the
+// MMAs' own time is 2048, and those of Q K, with both operands in shared memory, take all of its 128
+// bytes a cycle while the next tiles land there.  So the chain softmax -> P V -> Q K of a tile bounds
+// it, the other tile's MMAs filling its gaps; a second S per tile, which would cut the chain, does not
+// fit the tensor memory at head_dim 128.  Slower: two issuing warps, one a tile (343 us); 64-key halves
+// with S twice (304); both softmax groups on one tile with an exchange of maxima (292); all
+// exponentials on the MUFU pipe (282).
 #include <float.h>
 
 #include <type_traits>
