@@ -579,6 +579,37 @@ def test_attention_paged_and_write_far_into_a_cache(new):
         assert torch.equal(*outs) and torch.isfinite(outs[0]).all()
 
 
+@pytest.mark.parametrize("ids", [[0], [-1], [6], [2, 5], [3, 3], [-1, 4], [-2, 1]])
+@pytest.mark.parametrize("N,K,r", [(8, 8, 4), (296, 1024, 16), (1000, 264, 8), (304, 5120, 12), (20008, 40, 1),
+                                   (512, 8200, 256), (152, 20480, 64)])
+def test_linear_adapters_one_and_two_rows(ids, N, K, r):
+    """Ranges of W's rows that do not divide, K's tails, ranks, ids that name no adapter; bias, ReLU and
+    accumulate; an infinite factor of another adapter."""
+    from zeroth_order_fine_b200 import zo
+    M, n = len(ids), 6 if r != 1 else 8
+    x, W, A, B, idt, sc, b = adapt_case(M, N, K, n, r, ids, BF, seed=K)
+    ref, tol = adapt_ref(x, W, A, B, idt, sc, b, n, r, True, True)
+    own = [a for a in range(n) if a not in ids]
+    A[own[0] * r:(own[0] + 1) * r] = math.inf
+    B[:, own[-1] * r:(own[-1] + 1) * r] = math.inf
+    x, W, A, B, idt, sc, b = (t.cuda() for t in (x, W, A, B, idt, sc, b))
+    ok = [m for m in range(M) if -1 <= ids[m] < n]
+    for act in (0, 1):
+        y = zo.zo_op_linear_adapters(x, W, A, B, idt, sc, b, act=act).double().cpu()
+        want = ref.clamp(min=0) if act else ref
+        assert torch.all((y - want).abs()[ok] <= tol[ok])
+        assert all(torch.isnan(y[m]).all() for m in range(M) if m not in ok)
+    base = torch.randn(M, N, generator=torch.Generator().manual_seed(1))
+    out = base.cuda()
+    zo.zo_op_linear_adapters(x, W, A, B, idt, sc, b, accumulate=True, out=out)
+    got = out.double().cpu() - base.double()
+    slack = tol + 2 * U * (base.double().abs() + ref.abs())      # the fp32 sum's rounding
+    assert torch.all((got - ref).abs()[ok] <= slack[ok])
+    assert torch.equal(zo.zo_op_linear_adapters(x, W, A, B, idt, sc, b)[ok], zo.zo_op_linear_adapters(
+        x, W, A, B, idt, sc, b)[ok])
+    assert zo.zo_op_error_word() == 0
+
+
 @pytest.mark.parametrize("M", [5, 40, 300, 2500])
 def test_linear_adapters_of_65536_factor_columns(M):
     """The most adapters there can be; 2500 rows: two passes of the tiles form."""

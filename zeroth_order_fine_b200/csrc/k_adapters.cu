@@ -1,9 +1,10 @@
 // One linear layer for rows of many requests, each row under an adapter of its own:
 //   y[m] = act(x[m] W^T + b + scale[a] (x[m] A_a^T) B_a^T),  a = row_adapter[m].
 //
-// Tensor-core forms (bf16): the expand runs as extra K blocks of the product's tcgen05 GEMM, with the
+// Tensor-core forms (bf16, from three rows on): the expand runs as extra K blocks of the product's tcgen05 GEMM, with the
 // rows' shrink S masked to their own adapter (zeros in the others' columns); of the factors' 64-column
 // blocks, and of those the 16-column steps, only those that the rows at hand touch.
+//   one or two rows: no tensor cores, W streamed by CUDA cores with S beside it.
 //   decode steps (up to 128 rows): the product is a stream of W, the weights on the tensor cores'
 //     128-row side; S comes from a CUDA-core kernel beside its first blocks.
 //   more rows: per 256-row block a list of blocks, S from a tcgen05 shrink, 256 x 256 output tiles.
@@ -370,6 +371,175 @@ cudaError_t launch_shrink_rows(const AdapterArgs& a, __nv_bfloat16* S, int ldS, 
     return cudaGetLastError();
 }
 
+// ---- one or two rows ---------------------------------------------------------------------------
+// A decode step of one request is 2 flops per weight byte and row: CUDA cores stream W as fast as HBM
+// gives it, without the swapped product's splits, slices and tensor maps.  A CTA takes an equal range of
+// W's rows; the steps of that range (two rows by 1024 of K) are one line that its 16 warps share
+// equally, each with the next step's 8 KB in flight (64 KB an SM besides what it works on).  A row's
+// dots are summed over a warp's lanes together (each step halves what a lane holds) and over the warps
+// through shared memory in warp order, with fp32 sums throughout.  S, fp32, comes from a small kernel
+// beside it and is needed only at the end, where 8 threads take an output: the warps' sums, S B_a^T,
+// bias, activation.  HBM bounds it: 4096 x 4096, rank 16: 11.7 us (2.9 TB/s with launch and ramp),
+// 15360 x 5120: 29 us (5.4 TB/s).
+// One row against the swapped product, 4096 x 4096: 12.0 and 15.9 us, 15360 x 5120: 29 and 33, 5120 x
+// 20480: 36 and 43, 20480 x 5120 rank 64: 39 and 47; two rows: 14.0 and 15.8, 33.4 and 33.1, 40 and 43,
+// 44 and 47; four rows (17.7 and 16.1, 47 and 34, 57 and 43, 67 and 49) are the product's.
+constexpr int ROWS_MOST = 2;
+constexpr int ROW_WARPS = 16, ROW_PASS = 128;          // W rows between two looks at S
+
+__global__ void __launch_bounds__(SH_WARPS * 32) adapter_row_shrink_kernel(AdapterArgs a, float* __restrict__ S) {
+    __shared__ float parts[SH_WARPS];
+    grid_dep_launch();
+    const int m = blockIdx.x / a.rank, j = blockIdx.x % a.rank;
+    const int id = a.ids[m], lane = threadIdx.x & 31;
+    if (id < 0 || id >= a.n_adapters) return;
+    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + (size_t)m * a.K);
+    const uint4* f = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.A) +
+                                                    ((size_t)id * a.rank + j) * a.K);
+    float s[2] = {0.f, 0.f};
+#pragma unroll 4
+    for (int k = threadIdx.x; k < a.K / 8; k += SH_WARPS * 32) {
+        float xv[8], fv[8];
+        bf8(__ldg(x + k), xv);
+        bf8(__ldg(f + k), fv);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i & 1] = fmaf(xv[i], fv[i], s[i & 1]);
+    }
+    const float v = warp_sum(s[0] + s[1]);
+    if (lane == 0) parts[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float t = 0.f;
+        for (int w = 0; w < SH_WARPS; ++w) t += parts[w];
+        S[(size_t)m * a.rank + j] = t * a.scale[id];
+    }
+}
+
+__device__ __forceinline__ uint4 load_once(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+template <int MR>
+__global__ void __launch_bounds__(ROW_WARPS * 32, 1)
+    adapter_rows_kernel(AdapterArgs a, const float* __restrict__ S, int per) {
+    constexpr int RB = 2, U = 4, V = MR * RB;          // rows and 256-element chunks of K of a step
+    __shared__ float red[ROW_WARPS][ROW_PASS * MR];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, K8 = a.K / 8;
+    const int first = (int)blockIdx.x * per, last = min(a.N, first + per);
+    const int groups = (K8 + 32 * U - 1) / (32 * U);
+    const uint4* W = static_cast<const uint4*>(a.W);
+    const uint4* X = static_cast<const uint4*>(a.x);
+    const size_t ldb = (size_t)a.n_adapters * a.rank;
+    for (int p0 = first; p0 < last; p0 += ROW_PASS) {
+        const int rows = min(ROW_PASS, last - p0), line = (rows + RB - 1) / RB * groups;
+        const int share = (line + ROW_WARPS - 1) / ROW_WARPS;
+        const int s0 = min(line, warp * share), steps = min(line, s0 + share) - s0;
+        for (int i = lane; i < rows * MR; i += 32) red[warp][i] = 0.f;
+        __syncwarp();
+        uint4 w[2][RB * U];
+        int lr = s0 / groups * RB, lg = s0 % groups;   // the next load's rows and chunks
+        auto load = [&](uint4* to) {
+#pragma unroll
+            for (int i = 0; i < RB; ++i)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int k = (lg * U + u) * 32 + lane;
+                    to[i * U + u] = lr + i < rows && k < K8 ? load_once(W + (size_t)(p0 + lr + i) * K8 + k)
+                                                            : make_uint4(0u, 0u, 0u, 0u);
+                }
+            if (++lg == groups) {
+                lg = 0;
+                lr += RB;
+            }
+        };
+        int r = lr, g = lg;                            // the next step to use
+        float acc[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = 0.f;
+        auto use = [&](const uint4* from, bool end) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = (g * U + u) * 32 + lane;
+                float wv[RB][8];
+#pragma unroll
+                for (int i = 0; i < RB; ++i) bf8(from[i * U + u], wv[i]);
+#pragma unroll
+                for (int m = 0; m < MR; ++m) {
+                    float xv[8];
+                    bf8(k < K8 && m < a.M ? __ldg(X + (size_t)m * K8 + k) : make_uint4(0u, 0u, 0u, 0u), xv);
+#pragma unroll
+                    for (int i = 0; i < RB; ++i)
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) acc[i * MR + m] = fmaf(xv[q], wv[i][q], acc[i * MR + m]);
+                }
+            }
+            if (++g < groups && !end) return;
+            // the lanes' sums: a lane keeps the half of its dots that its bit of the step names
+            int at = 0;
+#pragma unroll
+            for (int n = V / 2, o = 16; o > 0; n >>= 1, o >>= 1) {
+                if (n > 0) {
+                    const bool hi = lane & o;
+                    at = at * 2 + (hi ? 1 : 0);
+#pragma unroll
+                    for (int i = 0; i < n; ++i) {
+                        const float send = hi ? acc[i] : acc[i + n], keep = hi ? acc[i + n] : acc[i];
+                        acc[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                    }
+                } else {
+                    acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
+                }
+            }
+            if (lane % (32 / V) == 0 && r + at / MR < rows) red[warp][r * MR + at] = acc[0];
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = 0.f;
+            g = 0;
+            r += RB;
+        };
+        if (steps > 0) load(w[0]);
+        for (int step = 0; step < steps; step += 2) {
+            if (step + 1 < steps) load(w[1]);
+            use(w[0], step + 1 == steps);
+            if (step + 1 < steps) {
+                if (step + 2 < steps) load(w[0]);
+                use(w[1], step + 2 == steps);
+            }
+        }
+        grid_dep_wait();                               // S
+        __syncthreads();
+        for (int q = tid >> 3; q < rows * MR; q += ROW_WARPS * 4) {
+            const int n = p0 + q / MR, m = q % MR, l8 = tid & 7;
+            const int id = m < a.M ? a.ids[m] : -1;
+            float v = red[l8][q] + red[l8 + 8][q];
+            if (id >= 0 && id < a.n_adapters) {
+                const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(a.B) + (size_t)n * ldb + (size_t)id * a.rank;
+                for (int j = l8; j < a.rank; j += 8)
+                    v = fmaf(S[(size_t)m * a.rank + j], __bfloat162float(b[j]), v);
+            }
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffu << (lane & 24), v, o);
+            if (id < -1 || id >= a.n_adapters) v = __int_as_float(0x7fc00000);
+            if (l8 == 0 && m < a.M) adapter_store(a, m, n, v);
+        }
+        __syncthreads();
+    }
+}
+
+template <int MR>
+cudaError_t launch_rows(const AdapterArgs& a, cudaStream_t st) {
+    float* S = static_cast<float*>(a.ws);
+    adapter_row_shrink_kernel<<<a.M * a.rank, SH_WARPS * 32, 0, st>>>(a, S);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int per = (a.N + 147) / 148;
+    return launch_pdl(adapter_rows_kernel<MR>, dim3(cdiv(a.N, per)), dim3(ROW_WARPS * 32), 0, st, a,
+                      static_cast<const float*>(S), per);
+}
+
 // The slices' reduction of the decode form: one thread per 4 columns of a row adds them in split
 // order, with bias and activation; sums that are not finite are taken anew from the row's own factors.
 __global__ void __launch_bounds__(128)
@@ -572,6 +742,7 @@ bool linear_adapters_tc_supported(const AdapterArgs& a) {
 }
 
 cudaError_t launch_linear_adapters_tc(const AdapterArgs& a, cudaStream_t st) {
+    if (a.M <= ROWS_MOST) return a.M == 1 ? launch_rows<1>(a, st) : launch_rows<2>(a, st);
     char* ws = static_cast<char*>(a.ws);
     const int K2 = a.n_adapters * a.rank;
     const TileSpace t = tile_space(a.M, a.N, K2);
