@@ -8,6 +8,7 @@ the import of any entry point raises: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Dict, List, Optional, Sequence
 
@@ -719,6 +720,12 @@ def _fits(dev: int, *checks) -> bool:
     return True
 
 
+@functools.lru_cache(maxsize=4096)
+def _workspace(op: str, *sizes) -> int:
+    """A *_workspace size: of the sizes alone, so a step that repeats them does not ask again."""
+    return int(getattr(lib(), op)(*sizes))
+
+
 def _dtype_id(dt: torch.dtype) -> int:
     return wl.DTYPE_BF16 if dt is torch.bfloat16 else wl.DTYPE_FP32
 
@@ -800,8 +807,8 @@ def zo_op_kv_write(qkv: torch.Tensor, slot_map: torch.Tensor, cache: torch.Tenso
 
 def zo_op_attention_paged_workspace(n_tokens: int, n_rows: int, n_heads: int, n_kv_heads: int,
                                     head_dim: int, dtype: torch.dtype = torch.bfloat16) -> int:
-    return int(lib().zo_op_attention_paged_workspace(n_tokens, n_rows, n_heads, n_kv_heads,
-                                                     head_dim, _dtype_id(dtype)))
+    return _workspace("zo_op_attention_paged_workspace", n_tokens, n_rows, n_heads, n_kv_heads,
+                      head_dim, _dtype_id(dtype))
 
 
 def zo_op_attention_paged(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
@@ -825,8 +832,8 @@ def zo_op_attention_paged(q: torch.Tensor, cache: torch.Tensor, block_table: tor
     if out.shape[0] != T or out.get_device() != dev:
         raise ValueError("out must have q's rows and device")
     if ws is None:
-        ws = torch.empty(L.zo_op_attention_paged_workspace(T, R, n_heads, n_kv_heads, head_dim, did),
-                         dtype=torch.uint8, device=q.device)
+        need = _workspace("zo_op_attention_paged_workspace", T, R, n_heads, n_kv_heads, head_dim, did)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
     kv2 = 2 * n_kv_heads * head_dim
     if not _fits(dev, (cache, dt, (cache.shape[0], kv2)), (block_table, i32, (R, max_blocks)),
                  (cu_new, i32, (R + 1,)), (lens, i32, (R,)), (ws, torch.uint8, ws.shape[:1])):
@@ -844,7 +851,7 @@ def zo_op_attention_paged(q: torch.Tensor, cache: torch.Tensor, block_table: tor
 
 def zo_op_linear_adapters_workspace(M: int, N: int, K: int, n_adapters: int, rank: int,
                                     dtype: torch.dtype = torch.bfloat16) -> int:
-    return int(lib().zo_op_linear_adapters_workspace(M, N, K, n_adapters, rank, _dtype_id(dtype)))
+    return _workspace("zo_op_linear_adapters_workspace", M, N, K, n_adapters, rank, _dtype_id(dtype))
 
 
 def zo_op_linear_adapters(x: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
@@ -868,7 +875,7 @@ def zo_op_linear_adapters(x: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: 
     if out is None:
         out = torch.empty(M, N, dtype=dt, device=x.device)
     if ws is None:
-        need = L.zo_op_linear_adapters_workspace(M, N, K, n_adapters, rank, did)
+        need = _workspace("zo_op_linear_adapters_workspace", M, N, K, n_adapters, rank, did)
         ws = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
     if not (dt in _FLOATS and
             _fits(dev, (x, dt, (M, K)), (W, dt, (N, K)), (A, dt, (K2, K)), (B, dt, (N, K2)),
