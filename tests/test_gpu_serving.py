@@ -282,6 +282,26 @@ def test_attention_paged_with_a_wrong_hint(max_new):
     c.check(c.run(max_new=max_new), 0)
 
 
+@pytest.mark.parametrize("old,new", [(300, 1), (0, 3), (77, 0), (5, 40), (2000, 5), (0, 700)])
+@pytest.mark.parametrize("lay", [(8, 2, 128), (6, 2, 64), (16, 1, 128)])
+@pytest.mark.parametrize("max_new", [1, 1000])
+def test_attention_paged_of_a_request_alone(old, new, lay, max_new):
+    """One request, whichever kernel the hint picks."""
+    c = Paged([(old, new)], *lay, 16, BF)
+    c.check(c.run(max_new=max_new), 0)
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_attention_paged_of_one_long_among_short(dt):
+    """An item of many pieces beside whole ones; tiles of every number of rows."""
+    reqs = [(4000, 1)] + [(r.randrange(0, 90), r.randrange(1, 6)) for r in [random.Random(4)] for _ in range(40)]
+    c = Paged(reqs, 4, 2, 64, 32, dt)
+    c.check(c.run(), 0 if dt == BF else 1)
+    reqs = [(900, n) for n in (8, 9, 16, 17, 32, 33, 64, 65)]
+    c = Paged(reqs, 2, 2, 64, 16, dt)
+    c.check(c.run(impl=1), 1)
+
+
 @pytest.mark.parametrize("dt,impl", [(BF, 0), (BF, 1), (FP, 1)])
 @pytest.mark.parametrize("kind", ["page", "page-negative", "short", "long", "rows"])
 def test_attention_paged_bad_requests(kind, dt, impl):
