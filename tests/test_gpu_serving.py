@@ -630,6 +630,34 @@ def test_linear_adapters_one_and_two_rows(ids, N, K, r):
     assert zo.zo_op_error_word() == 0
 
 
+@pytest.mark.parametrize("M,N,K,n,r", [(300, 8200, 264, 7, 16), (1500, 1544, 200, 9, 24), (1030, 512, 640, 5, 64),
+                                       (260, 1024, 64, 40, 8)])
+def test_linear_adapters_of_many_tiles(M, N, K, n, r):
+    """Batches above the decode form's: ids that name no adapter, an infinite factor of another adapter,
+    ReLU and accumulate."""
+    from zeroth_order_fine_b200 import zo
+    ids = spans(M, n - 1, M, 1, 90)
+    x, W, A, B, idt, sc, b = adapt_case(M, N, K, n, r, ids, BF, seed=M)
+    ref, tol = adapt_ref(x, W, A, B, idt, sc, b, n, r, True, True)
+    B[:, (n - 1) * r:] = math.inf
+    idt[7], idt[M - 1] = n, -5
+    bad = torch.zeros(M, dtype=torch.bool)
+    bad[7] = bad[M - 1] = True
+    x, W, A, B, idt, sc, b = (t.cuda() for t in (x, W, A, B, idt, sc, b))
+    for act in (0, 1):
+        y = zo.zo_op_linear_adapters(x, W, A, B, idt, sc, b, act=act).double().cpu()
+        want = ref.clamp(min=0) if act else ref
+        assert torch.all((y - want).abs()[~bad] <= tol[~bad])
+        assert torch.isnan(y[bad]).all()
+    base = torch.randn(M, N, generator=torch.Generator().manual_seed(1))
+    out = base.cuda()
+    zo.zo_op_linear_adapters(x, W, A, B, idt, sc, b, accumulate=True, out=out)
+    got = out.double().cpu() - base.double()
+    slack = tol + 2 * U * (base.double().abs() + ref.abs())      # the fp32 sum's rounding
+    assert torch.all((got - ref).abs()[~bad] <= slack[~bad])
+    assert zo.zo_op_error_word() == 0
+
+
 @pytest.mark.parametrize("M", [5, 40, 300, 2500])
 def test_linear_adapters_of_65536_factor_columns(M):
     """The most adapters there can be; 2500 rows: two passes of the tiles form."""

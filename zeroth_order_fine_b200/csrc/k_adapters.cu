@@ -5,7 +5,7 @@
 // rows' shrink S masked to their own adapter (zeros in the others' columns); of the factors' 64-column
 // blocks, and of those the 16-column steps, only those that the rows at hand touch.
 //   one or two rows: no tensor cores, W streamed by CUDA cores with S beside it.
-//   decode steps (up to 128 rows): the product is a stream of W, the weights on the tensor cores'
+//   decode steps (up to 128 rows, and more of small layers): the product is a stream of W, the weights on the tensor cores'
 //     128-row side; S comes from a CUDA-core kernel beside its first blocks.
 //   more rows: per 256-row block a list of blocks, S from a tcgen05 shrink, 256 x 256 output tiles.
 // An output that the zeros have made non-finite (0 times another adapter's infinity) is computed anew
@@ -301,11 +301,11 @@ __global__ void __launch_bounds__(SH_WARPS * 32)
     if (grp == 0) {
         for (int i = threadIdx.x; i < (n_list + 7) / 8; i += blockDim.x) steps[i] = 0u;
         __syncthreads();
-        if (threadIdx.x < a.M) {
-            const int r = a.ids[threadIdx.x];
+        for (int i = threadIdx.x; i < a.M; i += blockDim.x) {
+            const int r = a.ids[i];
             if (r >= 0 && r < a.n_adapters)
                 for (int s = r * a.rank / 16; s <= ((r + 1) * a.rank - 1) / 16; ++s)
-                    atomicOr(&steps[s >> 5], 1u << (s & 31));
+                    if (!((steps[s >> 5] >> (s & 31)) & 1u)) atomicOr(&steps[s >> 5], 1u << (s & 31));
         }
         __syncthreads();
         const int lo = live ? id * a.rank : 0, hi = live ? lo + a.rank : 0;
@@ -652,9 +652,17 @@ __global__ void __launch_bounds__(FIX_THREADS)
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Rows up to which the decode form is taken, the most it can (OPT-13B FFN input under 32 adapters of
-// rank 16: 64 rows 63 us, the tiles form 99; 128 rows 68 and 101).
-constexpr int STEP_ROWS = 128;
+// Where the decode form is taken: up to 128 rows, and up to 1024 while its 128 x 128 tiles are at most
+// one a SM and the factors' columns, all of whose listed blocks every tile goes through, no more than
+// K's.  It splits K over the SMs that the tiles leave idle; the tiles form has 256 x 256 tiles for SM
+// pairs and no split.  128 rows of the OPT-13B FFN input under 32 adapters of rank 16: 68 us, the tiles
+// form 101; under 8 adapters, 2048 x 2048: 256 rows 17 and 41, 1024 rows (128 tiles) 36 and 42; 4096 x
+// 4096: 256 rows 28 and 56, 512 rows (128 tiles) 43 and 57, 768 rows (192) 60 and 57; 6144 x 4096 under
+// 32: 384 rows (144) 43 and 59, 768 rows (288) 74 and 60; 15360 x 5120: 256 rows (240) 74 and 70.
+bool step_form(int M, int N, int K, int K2) {
+    if (M <= 128) return true;
+    return M <= 1024 && K2 <= K && (long long)((M + 127) / 128) * ((N + 127) / 128) <= 148;
+}
 
 // Slices of the decode form: room for up to 16 splits, 64 MB at most unless one slice is more.
 size_t slice_floats(int M, int N) {
@@ -695,7 +703,7 @@ size_t adapter_workspace(int M, int N, int K, int n_adapters, int rank, int dtyp
     if (M == 0) return s;
     if (dtype != E_BF16) return s + up256((size_t)f32_splits(M, N, K) * M * N * 4);
     size_t t = tile_space(M, N, n_adapters * rank).total;
-    if (M <= STEP_ROWS) t += up256(slice_floats(M, N) * 4);
+    if (step_form(M, N, K, n_adapters * rank)) t += up256(slice_floats(M, N) * 4);
     return t > s ? t : s;
 }
 
@@ -755,7 +763,7 @@ cudaError_t launch_linear_adapters_tc(const AdapterArgs& a, cudaStream_t st) {
     at.S = ws + t.s;
     at.ldS = t.ld;
     at.odd = reinterpret_cast<uint8_t*>(ws + t.odd);
-    if (a.M <= STEP_ROWS) {
+    if (step_form(a.M, a.N, a.K, K2)) {
         GemmArgs g;
         memset(&g, 0, sizeof(g));
         g.A = a.x; g.lda = a.K; g.a_type = E_BF16;

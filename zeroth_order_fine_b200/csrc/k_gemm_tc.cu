@@ -2031,7 +2031,8 @@ int effective_splits(int kb_main, int ks, int* kbs) {
 }
 
 // Decode-step GEMM on single SMs with the operands swapped: A = the weights [N x K] (128-row
-// tiles), B = the M <= 128 token rows (one N tile of 32, 64 or 128), likewise for the
+// tiles), B = the M <= 128 token rows (one N tile of 32, 64 or 128; under adapters M may be larger, in
+// N tiles of 128), likewise for the
 // extension blocks.  Each (weight tile, K split) item writes its fp32 slice transposed into
 // the workspace, then the split reduction applies g's epilogue.
 int gemm_tc_swapped(const GemmArgs& g, cudaStream_t st) {
@@ -2059,8 +2060,8 @@ int gemm_tc_swapped(const GemmArgs& g, cudaStream_t st) {
     // swapped sides: the weight rows' scales are the kernel's M side, the tokens' its N side
     p.a_scale = g.b_scale; p.b_scale = g.a_scale;
     p.n_m_blk = (g.N + BM - 1) / BM;
-    p.n_n_blk = 1;
-    p.n_tiles = p.n_m_blk;
+    p.n_n_blk = (g.M + bnt - 1) / bnt;       // (more than one: adapters only)
+    p.n_tiles = p.n_m_blk * p.n_n_blk;
     p.group_m = GROUP_M;
     p.epi = EPI_SPLIT_T;
     p.C = g.ws; p.ldc = g.N; p.c_type = E_F32;
@@ -2078,7 +2079,7 @@ int gemm_tc_swapped(const GemmArgs& g, cudaStream_t st) {
     // take the split count with the smaller bound, every split keeping at least 2 blocks.
     const int sms = num_sms();
     constexpr double SM_BW_REL = 1.25;
-    const double slice = g.M / 32.0;                 // 128 x M fp32 = M / 32 weight blocks
+    const double slice = std::min(g.M, 128) / 32.0;  // 128 x M fp32 = M / 32 weight blocks
     int ks = 1;
     double best = 1e300;
     for (int k = 1; k <= 16 && k <= std::max(1, p.kb_main / 2); ++k) {
@@ -2088,7 +2089,7 @@ int gemm_tc_swapped(const GemmArgs& g, cudaStream_t st) {
         const long long items = (long long)p.n_tiles * k;
         const long long rounds = (items + sms - 1) / sms;
         const double t_sm = (double)rounds * (kbs + slice) / SM_BW_REL;
-        const double t_hbm = ((double)p.n_tiles * p.kb_main + 2.0 * items * slice) / sms;
+        const double t_hbm = ((double)p.n_m_blk * p.kb_main + 2.0 * items * slice) / sms;
         const double cost = std::max(t_sm, t_hbm);
         if (cost < best * 0.98) {                    // a clear gain for each extra split
             best = cost;
@@ -2185,7 +2186,7 @@ int gemm_tc(const GemmArgs& g, cudaStream_t st) {
     // their few token rows take the swapped single-SM form.
     const bool bf16_ops = g.a_type == E_BF16 && g.b_type == E_BF16;
     const bool e4m3_ops = g.a_type == E_FP8 && g.b_type == E_FP8 && g.a_scale && g.b_scale;
-    if (g.ws && g.M <= 128 && (bf16_ops || e4m3_ops) && g.N % 4 == 0 &&
+    if (g.ws && (g.M <= 128 || g.adapt) && (bf16_ops || e4m3_ops) && g.N % 4 == 0 &&
         (g.epi == EPI_STORE || g.epi == EPI_STORE_RELU || g.epi == EPI_RESID ||
          g.epi == EPI_SWIGLU || g.epi == EPI_QKNR || g.epi == EPI_SHRINK))
         return gemm_tc_swapped(g, st);

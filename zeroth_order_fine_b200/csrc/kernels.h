@@ -155,7 +155,7 @@ struct GemmArgs {
     // EPI_STORE / EPI_QKNR with a split reduction: the reduction may also append the k|v
     // columns to the cache (sets *kv_done = 1; else the caller copies them)
     const KvAppend* kv_append; int* kv_done;
-    // decode steps under adapters (M <= 128, a workspace given): the extension blocks are the listed
+    // decode steps under adapters (a workspace given, any M): the extension blocks are the listed
     // ones of adapt_tiles; launched behind the kernel that writes its lists and S; bias, activation
     // and output are the adapters'
     const AdapterArgs* adapt; const AdapterTiles* adapt_tiles;
