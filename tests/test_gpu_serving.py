@@ -630,6 +630,35 @@ def test_linear_adapters_one_and_two_rows(ids, N, K, r):
     assert zo.zo_op_error_word() == 0
 
 
+@pytest.mark.parametrize("M", [1, 2, 3, 5, 8, 9, 16, 23, 24, 25])
+@pytest.mark.parametrize("N,K,r", [(1, 4, 1), (149, 516, 7), (1000, 2048, 16), (296, 8196, 256)])
+def test_linear_adapters_few_rows_in_fp32(M, N, K, r):
+    """Groups of rows that do not fill, ids that name no adapter, ReLU and accumulate."""
+    from zeroth_order_fine_b200 import zo
+    n = 5
+    ids = spans(M, n - 1, M + K, 1, 3)
+    x, W, A, B, idt, sc, b = adapt_case(M, N, K, n, r, ids, FP, seed=K)
+    ref, tol = adapt_ref(x, W, A, B, idt, sc, b, n, r, False, False)
+    B[:, (n - 1) * r:] = math.inf
+    bad = torch.zeros(M, dtype=torch.bool)
+    if M > 1:
+        idt[M - 1] = n
+        bad[M - 1] = True
+    x, W, A, B, idt, sc, b = (t.cuda() for t in (x, W, A, B, idt, sc, b))
+    for act in (0, 1):
+        y = zo.zo_op_linear_adapters(x, W, A, B, idt, sc, b, act=act)
+        assert torch.equal(y[~bad], zo.zo_op_linear_adapters(x, W, A, B, idt, sc, b, act=act)[~bad])
+        want = ref.clamp(min=0) if act else ref
+        assert torch.all((y.double().cpu() - want).abs()[~bad] <= tol[~bad])
+        assert torch.isnan(y[bad]).all()
+    base = torch.randn(M, N, generator=torch.Generator().manual_seed(1))
+    out = base.cuda()
+    zo.zo_op_linear_adapters(x, W, A, B, idt, sc, b, accumulate=True, out=out)
+    got = out.double().cpu() - base.double()
+    slack = tol + 2 * U * (base.double().abs() + ref.abs())      # the fp32 sum's rounding
+    assert torch.all((got - ref).abs()[~bad] <= slack[~bad])
+
+
 @pytest.mark.parametrize("M,N,K,n,r", [(300, 8200, 264, 7, 16), (1500, 1544, 200, 9, 24), (1030, 512, 640, 5, 64),
                                        (260, 1024, 64, 40, 8)])
 def test_linear_adapters_of_many_tiles(M, N, K, n, r):

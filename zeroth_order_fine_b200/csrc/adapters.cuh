@@ -41,12 +41,13 @@ __device__ inline float adapter_element(const AdapterArgs& a, const __nv_bfloat1
 }
 
 // bias and activation (a NaN stays) and the store of one element
+template <typename T = __nv_bfloat16>
 __device__ __forceinline__ void adapter_store(const AdapterArgs& a, int m, int n, float v) {
     if (a.bias) v += a.bias[n];
     if (a.act == 1) v = v < 0.f ? 0.f : v;
     const size_t at = (size_t)m * a.N + n;
     if (a.accumulate) static_cast<float*>(a.y)[at] += v;
-    else static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
+    else static_cast<T*>(a.y)[at] = static_cast<T>(v);          // to the nearest
 }
 
 }  // namespace zo

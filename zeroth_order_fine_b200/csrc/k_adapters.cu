@@ -4,7 +4,7 @@
 // Tensor-core forms (bf16, from three rows on): the expand runs as extra K blocks of the product's tcgen05 GEMM, with the
 // rows' shrink S masked to their own adapter (zeros in the others' columns); of the factors' 64-column
 // blocks, and of those the 16-column steps, only those that the rows at hand touch.
-//   one or two rows: no tensor cores, W streamed by CUDA cores with S beside it.
+//   one or two rows (fp32: up to 24): W streamed by CUDA cores with S beside it.
 //   decode steps (up to 128 rows, and more of small layers): the product is a stream of W, the weights on the tensor cores'
 //     128-row side; S comes from a CUDA-core kernel beside its first blocks.
 //   more rows: per 256-row block a list of blocks, S from a tcgen05 shrink, 256 x 256 output tiles.
@@ -371,39 +371,56 @@ cudaError_t launch_shrink_rows(const AdapterArgs& a, __nv_bfloat16* S, int ldS, 
     return cudaGetLastError();
 }
 
-// ---- one or two rows ---------------------------------------------------------------------------
-// A decode step of one request is 2 flops per weight byte and row: CUDA cores stream W as fast as HBM
-// gives it, without the swapped product's splits, slices and tensor maps.  A CTA takes an equal range of
-// W's rows; the steps of that range (two rows by 1024 of K) are one line that its 16 warps share
-// equally, each with the next step's 8 KB in flight (64 KB an SM besides what it works on).  A row's
-// dots are summed over a warp's lanes together (each step halves what a lane holds) and over the warps
-// through shared memory in warp order, with fp32 sums throughout.  S, fp32, comes from a small kernel
-// beside it and is needed only at the end, where 8 threads take an output: the warps' sums, S B_a^T,
-// bias, activation.  HBM bounds it: 4096 x 4096, rank 16: 11.7 us (2.9 TB/s with launch and ramp),
-// 15360 x 5120: 29 us (5.4 TB/s).
-// One row against the swapped product, 4096 x 4096: 12.0 and 15.9 us, 15360 x 5120: 29 and 33, 5120 x
-// 20480: 36 and 43, 20480 x 5120 rank 64: 39 and 47; two rows: 14.0 and 15.8, 33.4 and 33.1, 40 and 43,
+// ---- a few rows --------------------------------------------------------------------------------
+// A decode step of one request is 2 flops per weight and row: CUDA cores stream W as fast as HBM gives
+// it, without the swapped product's splits, slices and tensor maps.  A CTA takes an equal range of W's
+// rows; the steps of that range (two rows by 2 KB of K) are one line that its 16 warps share equally,
+// each with the next step's 4 KB in flight (64 KB an SM besides what it works on).  A row's dots are
+// summed over a warp's lanes together (each step halves what a lane holds) and over the warps through
+// shared memory in warp order, with fp32 sums throughout.  S, fp32, comes from a small kernel beside it
+// and is needed only at the end, where 8 threads take an output: the warps' sums, S B_a^T, bias,
+// activation.  HBM bounds it: bf16, 4096 x 4096, rank 16: 11.7 us (2.9 TB/s with launch and ramp), 15360
+// x 5120: 29 us (5.4 TB/s).
+// bf16, one row against the swapped product: 4096 x 4096 12.0 and 15.9 us, 15360 x 5120 29 and 33, 5120
+// x 20480 36 and 43, 20480 x 5120 rank 64 39 and 47; two rows: 14.0 and 15.8, 33.4 and 33.1, 40 and 43,
 // 44 and 47; four rows (17.7 and 16.1, 47 and 34, 57 and 43, 67 and 49) are the product's.
-constexpr int ROWS_MOST = 2;
-constexpr int ROW_WARPS = 16, ROW_PASS = 128;          // W rows between two looks at S
+// fp32, in groups of up to 8 rows, against the tiled product: 4096 x 4096, 1 row 16 and 71 us, 8 rows
+// 26 and 84, 24 rows 68 and 89, 32 rows 89 and 89; 2048 x 2048: 8.5 and 24, 13 and 29, 30 and 32, 38
+// and 33.
+constexpr int ROWS_MOST = 2, ROWS_MOST_F32 = 24;
+constexpr int ROW_WARPS = 16;
 
+// the elements of 16 bytes, in fp32
+template <typename T>
+__device__ __forceinline__ void floats_of(const uint4& u, float* f);
+template <>
+__device__ __forceinline__ void floats_of<__nv_bfloat16>(const uint4& u, float* f) { bf8(u, f); }
+template <>
+__device__ __forceinline__ void floats_of<float>(const uint4& u, float* f) {
+    f[0] = __uint_as_float(u.x);
+    f[1] = __uint_as_float(u.y);
+    f[2] = __uint_as_float(u.z);
+    f[3] = __uint_as_float(u.w);
+}
+
+template <typename T>
 __global__ void __launch_bounds__(SH_WARPS * 32) adapter_row_shrink_kernel(AdapterArgs a, float* __restrict__ S) {
     __shared__ float parts[SH_WARPS];
     grid_dep_launch();
     const int m = blockIdx.x / a.rank, j = blockIdx.x % a.rank;
     const int id = a.ids[m], lane = threadIdx.x & 31;
     if (id < 0 || id >= a.n_adapters) return;
-    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + (size_t)m * a.K);
-    const uint4* f = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.A) +
-                                                    ((size_t)id * a.rank + j) * a.K);
+    constexpr int E = 16 / sizeof(T);
+    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + (size_t)m * a.K);
+    const uint4* f = reinterpret_cast<const uint4*>(static_cast<const T*>(a.A) + ((size_t)id * a.rank + j) * a.K);
     float s[2] = {0.f, 0.f};
 #pragma unroll 4
-    for (int k = threadIdx.x; k < a.K / 8; k += SH_WARPS * 32) {
-        float xv[8], fv[8];
-        bf8(__ldg(x + k), xv);
-        bf8(__ldg(f + k), fv);
+    for (int k = threadIdx.x; k < a.K / E; k += SH_WARPS * 32) {
+        float xv[E], fv[E];
+        floats_of<T>(__ldg(x + k), xv);
+        floats_of<T>(__ldg(f + k), fv);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[i & 1] = fmaf(xv[i], fv[i], s[i & 1]);
+        for (int i = 0; i < E; ++i) s[i & 1] = fmaf(xv[i], fv[i], s[i & 1]);
     }
     const float v = warp_sum(s[0] + s[1]);
     if (lane == 0) parts[threadIdx.x >> 5] = v;
@@ -423,19 +440,21 @@ __device__ __forceinline__ uint4 load_once(const uint4* p) {
     return v;
 }
 
-template <int MR>
+template <typename T, int MR>
 __global__ void __launch_bounds__(ROW_WARPS * 32, 1)
     adapter_rows_kernel(AdapterArgs a, const float* __restrict__ S, int per) {
-    constexpr int RB = 2, U = 4, V = MR * RB;          // rows and 256-element chunks of K of a step
-    __shared__ float red[ROW_WARPS][ROW_PASS * MR];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, K8 = a.K / 8;
+    constexpr int RB = 2, U = 4, V = MR * RB;          // rows and 512-byte chunks of K of a step
+    constexpr int E = 16 / sizeof(T), PASS = MR <= 4 ? 128 : 64;      // W rows between two looks at S
+    __shared__ float red[ROW_WARPS][PASS * MR];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, KE = a.K / E;
+    const int m0 = (int)blockIdx.y * MR, mr = min(MR, a.M - m0);      // the CTA's rows of x
     const int first = (int)blockIdx.x * per, last = min(a.N, first + per);
-    const int groups = (K8 + 32 * U - 1) / (32 * U);
+    const int groups = (KE + 32 * U - 1) / (32 * U);
     const uint4* W = static_cast<const uint4*>(a.W);
     const uint4* X = static_cast<const uint4*>(a.x);
     const size_t ldb = (size_t)a.n_adapters * a.rank;
-    for (int p0 = first; p0 < last; p0 += ROW_PASS) {
-        const int rows = min(ROW_PASS, last - p0), line = (rows + RB - 1) / RB * groups;
+    for (int p0 = first; p0 < last; p0 += PASS) {
+        const int rows = min(PASS, last - p0), line = (rows + RB - 1) / RB * groups;
         const int share = (line + ROW_WARPS - 1) / ROW_WARPS;
         const int s0 = min(line, warp * share), steps = min(line, s0 + share) - s0;
         for (int i = lane; i < rows * MR; i += 32) red[warp][i] = 0.f;
@@ -448,7 +467,7 @@ __global__ void __launch_bounds__(ROW_WARPS * 32, 1)
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int k = (lg * U + u) * 32 + lane;
-                    to[i * U + u] = lr + i < rows && k < K8 ? load_once(W + (size_t)(p0 + lr + i) * K8 + k)
+                    to[i * U + u] = lr + i < rows && k < KE ? load_once(W + (size_t)(p0 + lr + i) * KE + k)
                                                             : make_uint4(0u, 0u, 0u, 0u);
                 }
             if (++lg == groups) {
@@ -464,17 +483,17 @@ __global__ void __launch_bounds__(ROW_WARPS * 32, 1)
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int k = (g * U + u) * 32 + lane;
-                float wv[RB][8];
+                float wv[RB][E];
 #pragma unroll
-                for (int i = 0; i < RB; ++i) bf8(from[i * U + u], wv[i]);
+                for (int i = 0; i < RB; ++i) floats_of<T>(from[i * U + u], wv[i]);
 #pragma unroll
                 for (int m = 0; m < MR; ++m) {
-                    float xv[8];
-                    bf8(k < K8 && m < a.M ? __ldg(X + (size_t)m * K8 + k) : make_uint4(0u, 0u, 0u, 0u), xv);
+                    float xv[E];
+                    floats_of<T>(k < KE && m < mr ? __ldg(X + (size_t)(m0 + m) * KE + k) : make_uint4(0u, 0u, 0u, 0u), xv);
 #pragma unroll
                     for (int i = 0; i < RB; ++i)
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) acc[i * MR + m] = fmaf(xv[q], wv[i][q], acc[i * MR + m]);
+                        for (int q = 0; q < E; ++q) acc[i * MR + m] = fmaf(xv[q], wv[i][q], acc[i * MR + m]);
                 }
             }
             if (++g < groups && !end) return;
@@ -513,30 +532,30 @@ __global__ void __launch_bounds__(ROW_WARPS * 32, 1)
         __syncthreads();
         for (int q = tid >> 3; q < rows * MR; q += ROW_WARPS * 4) {
             const int n = p0 + q / MR, m = q % MR, l8 = tid & 7;
-            const int id = m < a.M ? a.ids[m] : -1;
+            const int id = m < mr ? a.ids[m0 + m] : -1;
             float v = red[l8][q] + red[l8 + 8][q];
             if (id >= 0 && id < a.n_adapters) {
-                const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(a.B) + (size_t)n * ldb + (size_t)id * a.rank;
+                const T* b = static_cast<const T*>(a.B) + (size_t)n * ldb + (size_t)id * a.rank;
                 for (int j = l8; j < a.rank; j += 8)
-                    v = fmaf(S[(size_t)m * a.rank + j], __bfloat162float(b[j]), v);
+                    v = fmaf(S[(size_t)(m0 + m) * a.rank + j], (float)b[j], v);
             }
 #pragma unroll
             for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffu << (lane & 24), v, o);
             if (id < -1 || id >= a.n_adapters) v = __int_as_float(0x7fc00000);
-            if (l8 == 0 && m < a.M) adapter_store(a, m, n, v);
+            if (l8 == 0 && m < mr) adapter_store<T>(a, m0 + m, n, v);
         }
         __syncthreads();
     }
 }
 
-template <int MR>
+template <typename T, int MR>
 cudaError_t launch_rows(const AdapterArgs& a, cudaStream_t st) {
     float* S = static_cast<float*>(a.ws);
-    adapter_row_shrink_kernel<<<a.M * a.rank, SH_WARPS * 32, 0, st>>>(a, S);
+    adapter_row_shrink_kernel<T><<<a.M * a.rank, SH_WARPS * 32, 0, st>>>(a, S);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int per = (a.N + 147) / 148;
-    return launch_pdl(adapter_rows_kernel<MR>, dim3(cdiv(a.N, per)), dim3(ROW_WARPS * 32), 0, st, a,
+    return launch_pdl(adapter_rows_kernel<T, MR>, dim3(cdiv(a.N, per), cdiv(a.M, MR)), dim3(ROW_WARPS * 32), 0, st, a,
                       static_cast<const float*>(S), per);
 }
 
@@ -709,14 +728,21 @@ size_t adapter_workspace(int M, int N, int K, int n_adapters, int rank, int dtyp
 
 cudaError_t launch_linear_adapters_simt(const AdapterArgs& a, cudaStream_t st) {
     float* S = static_cast<float*>(a.ws);
+    const uintptr_t mix = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.W) |
+                          reinterpret_cast<uintptr_t>(a.A);
+    const bool rows16 = a.dtype == E_F32 && a.K % 4 == 0 && mix % 16 == 0;       // 16-byte loads
+    if (rows16 && a.M <= ROWS_MOST_F32)
+        return a.M == 1   ? launch_rows<float, 1>(a, st)
+               : a.M == 2 ? launch_rows<float, 2>(a, st)
+               : a.M <= 4 ? launch_rows<float, 4>(a, st)
+                          : launch_rows<float, 8>(a, st);
     static std::atomic<uint64_t> share{0};
     cudaError_t e = smem_share(reinterpret_cast<const void*>(adapter_shrink_kernel), share);
     if (e != cudaSuccess) return e;
     adapter_shrink_kernel<<<dim3(a.M, cdiv(a.rank, SH_WARPS)), SH_WARPS * 32, 0, st>>>(a, S);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const uintptr_t mix = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.W);
-    if (a.dtype == E_F32 && a.K % 4 == 0 && mix % 16 == 0) {
+    if (rows16) {
         static std::atomic<uint64_t> attr{0};
         e = smem_limit(reinterpret_cast<const void*>(gemm_f32_kernel), F_SMEM, attr);
         if (e != cudaSuccess) return e;
@@ -750,7 +776,8 @@ bool linear_adapters_tc_supported(const AdapterArgs& a) {
 }
 
 cudaError_t launch_linear_adapters_tc(const AdapterArgs& a, cudaStream_t st) {
-    if (a.M <= ROWS_MOST) return a.M == 1 ? launch_rows<1>(a, st) : launch_rows<2>(a, st);
+    if (a.M <= ROWS_MOST)
+        return a.M == 1 ? launch_rows<__nv_bfloat16, 1>(a, st) : launch_rows<__nv_bfloat16, 2>(a, st);
     char* ws = static_cast<char*>(a.ws);
     const int K2 = a.n_adapters * a.rank;
     const TileSpace t = tile_space(a.M, a.N, K2);
