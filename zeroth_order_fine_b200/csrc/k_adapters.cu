@@ -25,7 +25,9 @@ namespace {
 constexpr int SH_WARPS = 8;
 
 // S[m, j] for the rank rows of row m's own adapter: one warp per (m, j), the dot summed over the
-// lanes in a fixed tree.  Rows without an adapter are not written (nor read later).
+// lanes in a fixed tree.  Rows without an adapter are not written (nor read later).  VEC: fp32 with
+// 16-byte rows.
+template <bool VEC>
 __global__ void __launch_bounds__(SH_WARPS * 32) adapter_shrink_kernel(AdapterArgs a, float* S) {
     grid_dep_launch();                         // the fp32 product does not read S
     const int m = blockIdx.x, lane = threadIdx.x & 31;
@@ -35,7 +37,19 @@ __global__ void __launch_bounds__(SH_WARPS * 32) adapter_shrink_kernel(AdapterAr
     const size_t xr = (size_t)m * a.K, ar = ((size_t)id * a.rank + j) * a.K;
     const int t = a.dtype;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
-    int k = lane;
+    if (VEC) {
+        const float4* x = reinterpret_cast<const float4*>(static_cast<const float*>(a.x) + xr);
+        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(a.A) + ar);
+#pragma unroll 4
+        for (int q = lane; q < a.K / 4; q += 32) {
+            const float4 u = __ldg(x + q), v = __ldg(f + q);
+            s[0] = fmaf(u.x, v.x, s[0]);
+            s[1] = fmaf(u.y, v.y, s[1]);
+            s[2] = fmaf(u.z, v.z, s[2]);
+            s[3] = fmaf(u.w, v.w, s[3]);
+        }
+    }
+    int k = VEC ? a.K : lane;
     for (; k + 96 < a.K; k += 128)
 #pragma unroll
         for (int u = 0; u < 4; ++u)
@@ -228,6 +242,7 @@ __global__ void __launch_bounds__(128)
             for (int k = 0; k < ks; ++k) y[i] += slices[((size_t)k * a.M + m0 + i) * a.N + n];
     }
     const float* B = static_cast<const float*>(a.B) + (size_t)n * a.n_adapters * a.rank;
+    const bool vec = a.rank % 4 == 0 && reinterpret_cast<uintptr_t>(a.B) % 16 == 0;
 #pragma unroll
     for (int i = 0; i < ER; ++i) {
         // the run that begins at row i
@@ -235,7 +250,19 @@ __global__ void __launch_bounds__(128)
         int end = i + 1;
         while (end < rows && a.ids[m0 + end] == id[i]) ++end;
         const float* b = B + (size_t)id[i] * a.rank;
-        for (int c = 0; c < a.rank; ++c) {
+        int c = 0;
+        if (vec)
+#pragma unroll 4
+            for (; c < a.rank; c += 4) {
+                const float4 v = __ldg(reinterpret_cast<const float4*>(b + c));
+#pragma unroll
+                for (int q = i; q < ER; ++q) {
+                    if (q >= end) continue;
+                    const float4 f = *reinterpret_cast<const float4*>(&s[q][c]);
+                    y[q] = fmaf(f.w, v.w, fmaf(f.z, v.z, fmaf(f.y, v.y, fmaf(f.x, v.x, y[q]))));
+                }
+            }
+        for (; c < a.rank; ++c) {
             const float v = __ldg(b + c);
 #pragma unroll
             for (int q = i; q < ER; ++q)
@@ -726,6 +753,15 @@ size_t adapter_workspace(int M, int N, int K, int n_adapters, int rank, int dtyp
     return t > s ? t : s;
 }
 
+template <bool VEC>
+static cudaError_t launch_shrink(const AdapterArgs& a, float* S, cudaStream_t st) {
+    static std::atomic<uint64_t> share{0};
+    const cudaError_t e = smem_share(reinterpret_cast<const void*>(adapter_shrink_kernel<VEC>), share);
+    if (e != cudaSuccess) return e;
+    adapter_shrink_kernel<VEC><<<dim3(a.M, cdiv(a.rank, SH_WARPS)), SH_WARPS * 32, 0, st>>>(a, S);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_linear_adapters_simt(const AdapterArgs& a, cudaStream_t st) {
     float* S = static_cast<float*>(a.ws);
     const uintptr_t mix = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.W) |
@@ -736,11 +772,7 @@ cudaError_t launch_linear_adapters_simt(const AdapterArgs& a, cudaStream_t st) {
                : a.M == 2 ? launch_rows<float, 2>(a, st)
                : a.M <= 4 ? launch_rows<float, 4>(a, st)
                           : launch_rows<float, 8>(a, st);
-    static std::atomic<uint64_t> share{0};
-    cudaError_t e = smem_share(reinterpret_cast<const void*>(adapter_shrink_kernel), share);
-    if (e != cudaSuccess) return e;
-    adapter_shrink_kernel<<<dim3(a.M, cdiv(a.rank, SH_WARPS)), SH_WARPS * 32, 0, st>>>(a, S);
-    e = cudaGetLastError();
+    cudaError_t e = rows16 ? launch_shrink<true>(a, S, st) : launch_shrink<false>(a, S, st);
     if (e != cudaSuccess) return e;
     if (rows16) {
         static std::atomic<uint64_t> attr{0};
