@@ -306,7 +306,7 @@ int zo_op_attention_paged(const void* q, int64_t ld_q, const void* cache, int64_
  *   ws   dev, 256-byte aligned, >= zo_op_linear_adapters_workspace(...) bytes; scratch, not to
  *        be shared by calls that may run at the same time
  *   impl ZO_IMPL_TENSOR_CORES needs dtype bf16, K, N and n_adapters * rank multiples of 8 and
- *        16-byte aligned pointers; AUTO picks it then, else CUDA cores
+ *        16-byte aligned pointers; AUTO picks it then for three rows and more, else CUDA cores
  * M = 0 is a no-op.  ZO_ERR_ARG on NULL pointers, negative or empty sizes, rank above 256 or
  * n_adapters * rank above 65536, an unknown act, or a workspace too small or not aligned;
  * ZO_ERR_UNSUPPORTED for M above 4194240. */

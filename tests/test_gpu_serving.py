@@ -630,6 +630,16 @@ def test_linear_adapters_one_and_two_rows(ids, N, K, r):
     assert zo.zo_op_error_word() == 0
 
 
+@pytest.mark.parametrize("M", [1, 2])
+def test_linear_adapters_one_and_two_rows_on_the_tensor_cores(M):
+    from zeroth_order_fine_b200 import zo
+    x, W, A, B, idt, sc, b = adapt_case(M, 520, 1032, 5, 16, [3, -1][:M], BF, seed=M)
+    y = zo.zo_op_linear_adapters(x.cuda(), W.cuda(), A.cuda(), B.cuda(), idt.cuda(), sc.cuda(), b.cuda(), impl=2)
+    ref, tol = adapt_ref(x, W, A, B, idt, sc, b, 5, 16, True, True)
+    assert torch.all((y.double().cpu() - ref).abs() <= tol)
+    assert zo.zo_op_error_word() == 0
+
+
 @pytest.mark.parametrize("M", [1, 2, 3, 5, 8, 9, 16, 23, 24, 25])
 @pytest.mark.parametrize("N,K,r", [(1, 4, 1), (149, 516, 7), (1000, 2048, 16), (296, 8196, 256)])
 def test_linear_adapters_few_rows_in_fp32(M, N, K, r):

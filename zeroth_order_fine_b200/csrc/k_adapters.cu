@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(256) adapter_gemm_kernel(AdapterArgs a, const 
 
 // ---- fp32 -----------------------------------------------------------------------------------
 // The product in fp32 on CUDA cores, bound by their FMA rate (2 M N K flops at ~70 TFLOP/s; 301 x 2048 x
-// 2048 with its adapters 76 us, of which this kernel ~65: the FMA pipe is 63 % busy while an SM works
+// 2048 with its adapters 74 us, of which this kernel ~65: the FMA pipe is 63 % busy while an SM works
 // and the SMs work 91 % of the time; 48-byte spills at 128 registers for a fourth CTA gave nothing): 64 x 64
 // tiles, 8 x 4 outputs a thread, K in 32-deep stages by asynchronous 16-byte copies.  The tiles stay
 // as they lie in memory (K contiguous, rows padded to 36 floats): a thread reads 4 of K at a time of
@@ -807,8 +807,8 @@ bool linear_adapters_tc_supported(const AdapterArgs& a) {
            mix % 16 == 0;
 }
 
-cudaError_t launch_linear_adapters_tc(const AdapterArgs& a, cudaStream_t st) {
-    if (a.M <= ROWS_MOST)
+cudaError_t launch_linear_adapters_tc(const AdapterArgs& a, cudaStream_t st, bool few) {
+    if (few && a.M <= ROWS_MOST)
         return a.M == 1 ? launch_rows<__nv_bfloat16, 1>(a, st) : launch_rows<__nv_bfloat16, 2>(a, st);
     char* ws = static_cast<char*>(a.ws);
     const int K2 = a.n_adapters * a.rank;

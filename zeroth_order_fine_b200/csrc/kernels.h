@@ -240,7 +240,8 @@ int paged_chunk_error_word();
 size_t adapter_workspace(int M, int N, int K, int n_adapters, int rank, int dtype);
 cudaError_t launch_linear_adapters_simt(const AdapterArgs& a, cudaStream_t st);
 bool linear_adapters_tc_supported(const AdapterArgs& a);
-cudaError_t launch_linear_adapters_tc(const AdapterArgs& a, cudaStream_t st);
+// few: one or two rows may take the CUDA cores' streaming form
+cudaError_t launch_linear_adapters_tc(const AdapterArgs& a, cudaStream_t st, bool few);
 // y rows from ks fp32 slices ws[ks][M][N], bias and activation; pdl: a programmatic dependent of the
 // kernel that wrote the slices
 cudaError_t launch_adapter_reduce(const AdapterArgs& a, const AdapterTiles& t, const float* ws, int ks,

@@ -421,7 +421,7 @@ int zo_op_linear_adapters(const void* x, const void* W, const float* bias, const
     a.act = act; a.accumulate = accumulate;
     a.ws = ws; a.ws_bytes = ws_bytes;
     if (impl != ZO_IMPL_CUDA_CORES && linear_adapters_tc_supported(a)) {
-        if (launch_linear_adapters_tc(a, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        if (launch_linear_adapters_tc(a, static_cast<cudaStream_t>(stream), impl == ZO_IMPL_AUTO) != cudaSuccess)
             return op_fail("adapter linear launch failed");
         return ZO_OK;
     }
