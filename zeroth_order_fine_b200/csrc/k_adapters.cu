@@ -780,8 +780,18 @@ cudaError_t launch_linear_adapters_simt(const AdapterArgs& a, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         float* slices = reinterpret_cast<float*>(static_cast<char*>(a.ws) + up256((size_t)a.M * a.rank * 4));
         const int ks = f32_splits(a.M, a.N, a.K);
-        e = launch_pdl(gemm_f32_kernel, dim3(cdiv(a.N, FM), cdiv(a.M, FM), ks), dim3(F_THREADS), F_SMEM, st,
-                       static_cast<const float*>(a.x), static_cast<const float*>(a.W), a.M, a.N, a.K, ks, slices);
+        // The product beside the shrink, unless the shrink is long: then the two fight for L1 and the
+        // shrink reads x again and again from L2 (301 rows, 1544 x 1000: rank 8 45 us beside and 48
+        // behind, rank 64 100 and 66; 2048 x 2048, rank 32: 84 and 88, with adapters changing from row to
+        // row 107 and 103).
+        const dim3 grid(cdiv(a.N, FM), cdiv(a.M, FM), ks);
+        const float *x = static_cast<const float*>(a.x), *W = static_cast<const float*>(a.W);
+        if (a.N >= 64 * a.rank) {
+            e = launch_pdl(gemm_f32_kernel, grid, dim3(F_THREADS), F_SMEM, st, x, W, a.M, a.N, a.K, ks, slices);
+        } else {
+            gemm_f32_kernel<<<grid, F_THREADS, F_SMEM, st>>>(x, W, a.M, a.N, a.K, ks, slices);
+            e = cudaGetLastError();
+        }
         if (e != cudaSuccess) return e;
         return launch_pdl(adapter_expand_f32_kernel, dim3(cdiv(a.M, ER), cdiv(a.N, 128)), dim3(128), 0, st, a,
                           static_cast<const float*>(S), static_cast<const float*>(slices), ks);
