@@ -699,15 +699,18 @@ __global__ void __launch_bounds__(FIX_THREADS)
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Where the decode form is taken: up to 128 rows, and up to 1024 while its 128 x 128 tiles are at most
-// one a SM and the factors' columns, all of whose listed blocks every tile goes through, no more than
-// K's.  It splits K over the SMs that the tiles leave idle; the tiles form has 256 x 256 tiles for SM
+// one a SM, the factors' columns, all of whose listed blocks every tile goes through, no more than K's,
+// and the shrink, here on CUDA cores, 24576 dots at most.  It splits K over the SMs that the tiles leave idle; the tiles form has 256 x 256 tiles for SM
 // pairs and no split.  128 rows of the OPT-13B FFN input under 32 adapters of rank 16: 68 us, the tiles
 // form 101; under 8 adapters, 2048 x 2048: 256 rows 17 and 41, 1024 rows (128 tiles) 36 and 42; 4096 x
 // 4096: 256 rows 28 and 56, 512 rows (128 tiles) 43 and 57, 768 rows (192) 60 and 57; 6144 x 4096 under
-// 32: 384 rows (144) 43 and 59, 768 rows (288) 74 and 60; 15360 x 5120: 256 rows (240) 74 and 70.
-bool step_form(int M, int N, int K, int K2) {
+// 32: 384 rows (144) 43 and 59, 768 rows (288) 74 and 60; 15360 x 5120: 256 rows (240) 74 and 70.  By
+// the dots, 4096 x 4096 under rank 64: 384 rows (24576) 52 and 58, 512 rows (32768) 65 and 59; 2048 x
+// 2048, rank 32: 768 rows (24576) 37 and 43, 1024 rows (32768) 45 and 43.
+bool step_form(int M, int N, int K, int K2, int rank) {
     if (M <= 128) return true;
-    return M <= 1024 && K2 <= K && (long long)((M + 127) / 128) * ((N + 127) / 128) <= 148;
+    return M <= 1024 && M * rank <= 24576 && K2 <= K &&
+           (long long)((M + 127) / 128) * ((N + 127) / 128) <= 148;
 }
 
 // Slices of the decode form: room for up to 16 splits, 64 MB at most unless one slice is more.
@@ -749,7 +752,7 @@ size_t adapter_workspace(int M, int N, int K, int n_adapters, int rank, int dtyp
     if (M == 0) return s;
     if (dtype != E_BF16) return s + up256((size_t)f32_splits(M, N, K) * M * N * 4);
     size_t t = tile_space(M, N, n_adapters * rank).total;
-    if (step_form(M, N, K, n_adapters * rank)) t += up256(slice_floats(M, N) * 4);
+    if (step_form(M, N, K, n_adapters * rank, rank)) t += up256(slice_floats(M, N) * 4);
     return t > s ? t : s;
 }
 
@@ -832,7 +835,7 @@ cudaError_t launch_linear_adapters_tc(const AdapterArgs& a, cudaStream_t st, boo
     at.S = ws + t.s;
     at.ldS = t.ld;
     at.odd = reinterpret_cast<uint8_t*>(ws + t.odd);
-    if (step_form(a.M, a.N, a.K, K2)) {
+    if (step_form(a.M, a.N, a.K, K2, a.rank)) {
         GemmArgs g;
         memset(&g, 0, sizeof(g));
         g.A = a.x; g.lda = a.K; g.a_type = E_BF16;
