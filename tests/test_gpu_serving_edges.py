@@ -1,0 +1,112 @@
+"""The serving ops at contents and settings that a server meets rarely: keys and values that are not
+finite where a request sees them, and the other ends of what the calls promise.
+
+Bounds as in test_gpu_serving.py (u = 2^-24, h = 2^-8), with one term more: a weight of the chunk
+kernel may come from its own polynomial for 2^x, whose relative error is at most 2.7e-6, and a score
+of that kernel is scaled and shifted in one rounding.  A weight and the sum of the weights are off by
+that much each, an output by 2 * 2.7e-6 * sum w |v|.
+"""
+import math
+
+import pytest
+import torch
+
+from gpu_util import needs_gpu
+from test_gpu_serving import BF, FP, H, U, Paged, i32
+
+pytestmark = [pytest.mark.gpu, needs_gpu]
+
+POLY = 2.7e-6
+NAN, INF = float("nan"), float("inf")
+
+
+def set_key(c, r, i, col, x):
+    """Element col of token i's cache row (k, then v) of request r, in the cache and in the model."""
+    c.cache[c.table[r][i // c.p] * c.p + i % c.p, col] = x
+    c.kv[r][i, col] = x
+
+
+def compare(c, out, impl, may_be_nan=None):
+    """Every row against the definition in float64 (of finite values): NaN where that is NaN, else within
+    the bound.  may_be_nan[r]: rows of request r (by their new token) that may be NaN although they need not be."""
+    out, g, n_nan = out.double().cpu(), c.Hq // c.Hkv, 0
+    for r, (a, b) in enumerate(c.reqs):
+        n, hd = a + b, c.hd
+        rows = c.kv[r].double().view(n, 2, c.Hkv, hd)
+        q = c.q[c.cu[r]:c.cu[r + 1], :c.Hq * hd].double().view(b, c.Hq, hd)
+        unseen = torch.ones(b, n, dtype=torch.bool).triu(a + 1)
+        for h in range(c.Hq):
+            k, v = rows[:, 0, h // g], rows[:, 1, h // g]
+            s = (q[:, h] @ k.T / math.sqrt(hd)).masked_fill(unseen, -INF)
+            w = torch.softmax(s, -1)
+            ref, mag = w @ v, w @ v.abs()
+            kf = torch.where(k.isfinite(), k, torch.zeros((), dtype=torch.float64))
+            e = 2 * (hd + 3) * U * q[:, h].norm(dim=1) * kf.norm(dim=1).max() / math.sqrt(hd)
+            rel = 4 * e[:, None] + 3 * (n + 8) * U + 2 * POLY
+            if c.dt == BF:
+                rel = rel + (H if impl != 1 else 0.0)
+            tol = rel * mag + (H * ref.abs() if c.dt == BF else 0.0)
+            got = out[c.cu[r]:c.cu[r + 1], h * hd:(h + 1) * hd]
+            nan = ref.isnan()
+            n_nan += int(nan.sum())
+            assert got[nan].isnan().all(), (r, h, "finite where the definition has NaN")
+            fine = ~nan & ((got - ref).abs() <= tol)
+            if may_be_nan is not None:
+                fine |= got.isnan() & may_be_nan[r][:, None]
+            assert (fine | nan).all(), (r, h, (got - ref).abs()[~nan].max())
+    return n_nan
+
+
+# (new tokens of each request, types, impl): the step kernel, the chunk kernel, CUDA cores
+KERNELS = [(1, BF, 0), (200, BF, 0), (200, BF, 1), (9, FP, 1)]
+
+
+@pytest.mark.parametrize("what", [NAN, INF, -INF])
+@pytest.mark.parametrize("lay", [(8, 4, 128), (8, 4, 64)])
+@pytest.mark.parametrize("new,dt,impl", KERNELS)
+@pytest.mark.parametrize("at", ["early", "new"])
+def test_a_key_that_is_not_finite(new, dt, impl, lay, what, at):
+    """One such key at each of 16 places in a row: rows that see a NaN score or one of +infinity are
+    NaN, a score of -infinity has no weight, and rows that do not see the key are as without it."""
+    if at == "new" and new < 100:
+        pytest.skip("few new tokens")
+    c = Paged([(300, new)] * 16, *lay, 16, dt)
+    hd = lay[2]
+    c.q[:, ::hd] = c.q[:, ::hd].abs() + 0.5           # what x 0 would be NaN
+    for r in range(16):
+        set_key(c, r, (32 if at == "early" else 364) + r, hd * (r % 4), what)
+    n_nan = compare(c, c.run(impl), impl)
+    assert (n_nan > 0) == (what != -INF)
+
+
+@pytest.mark.parametrize("lay", [(8, 4, 128), (8, 4, 64)])
+@pytest.mark.parametrize("new,dt,impl", KERNELS)
+@pytest.mark.parametrize("reqs", [1, 16])
+def test_all_keys_at_minus_infinity(new, dt, impl, lay, reqs):
+    """No score is above -infinity: 0 / 0 in the rows of that kv head, whole items and cut ones."""
+    c = Paged([(300, new)] * reqs, *lay, 16, dt)
+    hd = lay[2]
+    c.q[:, ::hd] = c.q[:, ::hd].abs() + 0.5
+    for i in range(300 + new):
+        set_key(c, 0, i, hd, -INF)
+    assert compare(c, c.run(impl), impl) == new * 2 * hd
+
+
+@pytest.mark.parametrize("lay", [(8, 4, 128), (8, 4, 64)])
+@pytest.mark.parametrize("new,dt,impl", KERNELS)
+def test_a_value_that_is_not_finite(new, dt, impl, lay):
+    """Rows that see it take it over; rows before it may be NaN (0 times it)."""
+    c = Paged([(300, new)] * 4, *lay, 16, dt)
+    hd = lay[2]
+    for r, x in enumerate((NAN, INF, -INF, NAN)):
+        set_key(c, r, 300 + new // 2 if r < 3 else 40, (4 + r) * hd + 3, x)
+    seen = torch.arange(new) >= new // 2
+    out = c.run(impl).double().cpu()
+    for r in range(4):
+        col = 2 * r * hd + 3
+        got = out[c.cu[r]:c.cu[r + 1], [col, col + hd]]
+        rows = seen if r < 3 else torch.ones(new, dtype=torch.bool)
+        assert not got[rows].isfinite().any(), r
+        # the other columns and heads are not touched
+        clean = [x for x in range(c.Hq * hd) if x not in (col, col + hd)]
+        assert out[c.cu[r]:c.cu[r + 1], clean].isfinite().all()

@@ -201,6 +201,12 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// the larger of two, NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 // two fp32 operations in one instruction, each rounded as by itself
 __device__ __forceinline__ uint64_t pair(float a, float b) {
     uint64_t r;
@@ -222,7 +228,8 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-// 2^x of two values on the FMA pipe, for x >= -126 (below: 2^-126), relative error 2.7e-6: x = n + f with
+// 2^x of two values on the FMA pipe, for x >= -126 (below, and for NaN: 2^-126; the caller looks for
+// scores that are NaN or infinite by their maximum), relative error 2.7e-6: x = n + f with
 // n the nearest integer (from the low mantissa bits of x + 1.5 2^23), 2^f on [-1/2, 1/2] by the
 // degree-4 polynomial of least maximal relative error (fitted by linear programming over a
 // Chebyshev grid), n added to its exponent.
@@ -572,7 +579,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                             for (int j = 0; j < 16; j += 2) {
                                 const float s0 = __uint_as_float(v[j]), s1 = __uint_as_float(v[j + 1]);
-                                mx[(j >> 1) & 3] = fmaxf(mx[(j >> 1) & 3], fmaxf(s0, s1));
+                                mx[(j >> 1) & 3] = max_nan(mx[(j >> 1) & 3], max_nan(s0, s1));
                                 const float2 x = unpair(fma2(pair(s0, s1), c2, m2));
                                 const float2 e = !mask && on_fma(j) ? exp2_fma(x) : make_float2(ex2(x.x), ex2(x.y));
                                 ln[(j >> 1) & 3] = add2(ln[(j >> 1) & 3], pair(e.x, e.y));
@@ -582,7 +589,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                     };
                     if (masked) pass(std::true_type{});
                     else pass(std::false_type{});
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+                    // NaN if any score is, and then the row's result, as with a score of +infinity
+                    const float top = max_nan(max_nan(mx[0], mx[1]), max_nan(mx[2], mx[3])) * sl2;
+                    bad |= !(top < INFINITY);
                     const bool move = top > m + 8.f;
                     if (!__any_sync(0xffffffffu, move)) break;
                     const float mn = move ? top : m;
@@ -640,7 +649,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             const bool whole = done.c0 == 0 && done.c1 == it.units;
             const float2 l2 = unpair(add2(add2(l[0], l[1]), add2(l[2], l[3])));
-            const float lt = bad ? __int_as_float(0x7fc00000) : l2.x + l2.y;
+            // m still at its start: no score of the piece is above -infinity, and what the exponentials on
+            // the FMA pipe have left in l is no weight (a whole item's row is then 0 / 0)
+            const float lt = bad || (whole && m == -FLT_MAX) ? __int_as_float(0x7fc00000)
+                             : m == -FLT_MAX                 ? 0.f
+                                                             : l2.x + l2.y;
             Part<HD>* slot = part + 2 * w + (done.c0 == 0 ? 1 : 0);
             if (!whole) {
                 slot->m[t * 128 + row] = m;
