@@ -110,3 +110,33 @@ def test_a_value_that_is_not_finite(new, dt, impl, lay):
         # the other columns and heads are not touched
         clean = [x for x in range(c.Hq * hd) if x not in (col, col + hd)]
         assert out[c.cu[r]:c.cu[r + 1], clean].isfinite().all()
+
+
+@pytest.mark.parametrize("e", [8, 22, 31, 37, 60])
+@pytest.mark.parametrize("lay", [(8, 4, 128), (8, 4, 64)])
+@pytest.mark.parametrize("new,dt,impl", KERNELS)
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_of_any_size(new, dt, impl, lay, e, sign):
+    """Scores around 2^e of either sign, every factor with all its bits: the softmax goes to the largest,
+    which is far above the others, and its value row comes out.  One term of q.k is not zero, so a
+    product's error is its own rounding's."""
+    c = Paged([(300, new)] * 5, *lay, 16, dt)
+    Hq, Hkv, hd = lay
+    kmax = torch.tensor(2.0 ** (e - e // 2)).to(dt).item()
+    c.q[:, :Hq * hd] = 0
+    c.q[:, 0:Hq * hd:hd] = sign * 1.2890625 * 2.0 ** (e // 2)
+    g = torch.Generator().manual_seed(e)
+    for r in range(5):
+        k = torch.zeros(300 + new, Hkv, hd)
+        k[:, :, 0] = (1 + torch.rand(300 + new, Hkv, generator=g)) * kmax
+        k[70 + r, :, 0] = kmax * (2.609375 if sign > 0 else 0.3359375)
+        c.kv[r][:, :Hkv * hd] = k.view(300 + new, Hkv * hd).to(dt)
+        for i in range(300 + new):
+            c.cache[c.table[r][i // 16] * 16 + i % 16] = c.kv[r][i]
+    out = c.run(impl).double().cpu()
+    for r in range(5):
+        v = c.kv[r][70 + r, Hkv * hd:].double().view(Hkv, 1, hd).expand(Hkv, Hq // Hkv, hd).reshape(Hq * hd)
+        # 0.609 * 1.289 2^e / sqrt(hd) and more between the largest score and the others (|v| < 6)
+        others = (300 + new) * 12 * math.exp(-0.75 * 2.0 ** e / math.sqrt(hd))
+        tol = v.abs() * (2 * H if dt == BF else 2.0 ** -20) + others
+        assert ((out[c.cu[r]:c.cu[r + 1]] - v).abs() <= tol).all()

@@ -223,6 +223,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -535,7 +540,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (p.any(t)) load_q(k);
         while (ok) {
             const Line::Cursor it = k;
-            float m = -FLT_MAX;
+            float m = -FLT_MAX, raw = -FLT_MAX;       // the reference, scaled and as a score
             uint64_t l[4] = {0ull, 0ull, 0ull, 0ull};  // eight running sums
             bool bad = it.q.bad;
             const int r = it.tile * RB + t * 128 + row;
@@ -555,11 +560,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                 // (a piece's first unit, rarely later) does it move, and the pass is repeated; the
                 // scores are still there, since P goes out at the end.
                 const int cut = lim - c * UK;
-                const bool masked = !__all_sync(0xffffffffu, cut >= UK);
                 uint32_t pk[64];
                 uint64_t ln[4];
                 for (;;) {
-                    const uint64_t m2 = pair(-m, -m);
+                    // The usual pass scales a score and takes the reference off in one rounding.  The
+                    // reference has its own, which with scores of 2^31 and more is over 2^7 in the
+                    // exponent: no weight left, or none finite.  So the other pass, the one with the masks, takes
+                    // the reference off before it scales.
+                    const bool plain = cut >= UK && (fabsf(m) <= 0x1p20f || m == -FLT_MAX);
+                    const bool masked = !__all_sync(0xffffffffu, plain);
+                    const uint64_t m2 = pair(-m, -m), r2 = pair(-raw, -raw);
                     uint32_t sv[2][16];
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -580,7 +590,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             for (int j = 0; j < 16; j += 2) {
                                 const float s0 = __uint_as_float(v[j]), s1 = __uint_as_float(v[j + 1]);
                                 mx[(j >> 1) & 3] = max_nan(mx[(j >> 1) & 3], max_nan(s0, s1));
-                                const float2 x = unpair(fma2(pair(s0, s1), c2, m2));
+                                const float2 x = unpair(mask ? mul2(add2(pair(s0, s1), r2), c2) : fma2(pair(s0, s1), c2, m2));
                                 const float2 e = !mask && on_fma(j) ? exp2_fma(x) : make_float2(ex2(x.x), ex2(x.y));
                                 ln[(j >> 1) & 3] = add2(ln[(j >> 1) & 3], pair(e.x, e.y));
                                 pk[h * 8 + j / 2] = pack2(e.x, e.y);
@@ -590,7 +600,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (masked) pass(std::true_type{});
                     else pass(std::false_type{});
                     // NaN if any score is, and then the row's result, as with a score of +infinity
-                    const float top = max_nan(max_nan(mx[0], mx[1]), max_nan(mx[2], mx[3])) * sl2;
+                    const float most = max_nan(max_nan(mx[0], mx[1]), max_nan(mx[2], mx[3])), top = most * sl2;
                     bad |= !(top < INFINITY);
                     const bool move = top > m + 8.f;
                     if (!__any_sync(0xffffffffu, move)) break;
@@ -613,6 +623,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) l[i] = fma2(l[i], f2, 0ull);
                     m = mn;
+                    if (move) raw = most;
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) l[i] = ln[i];

@@ -361,7 +361,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[nb][e] = (s[nb][e] + s1[nb][e]) * sl2;
+            for (int e = 0; e < 4; ++e)               // (rounded by itself, as the reference is, whatever its size)
+                s[nb][e] = __fmul_rn(s[nb][e] + s1[nb][e], sl2);
         if (kbase + UK > lim_min) {
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
