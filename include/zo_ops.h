@@ -130,8 +130,8 @@ int zo_op_linear_ext(const void* x, const void* W, const float* bias, const void
 int zo_op_rope_table(float* cos_t, float* sin_t, int32_t max_pos, int32_t head_dim,
                      double theta, void* stream);
 
-/* Test hook for the failure path of the tensor-core GEMM kernels.  Every mbarrier wait in
- * them gives up after `cycles` SM clock cycles: the kernel then sets bit 0 of the error
+/* Test hook for the failure path of the tensor-core GEMM kernels and of the tensor-core
+ * kernels of zo_op_attention_paged.  Every mbarrier wait in them gives up after `cycles` SM clock cycles: the kernel then sets bit 0 of the error
  * word (zo_op_error_word), stops issuing work, waits (again with a bound) for the copies
  * and MMAs it has already issued, frees its tensor memory and returns; its output is
  * invalid.  The default bound, about 2 s, is far beyond any wait of a healthy launch; a

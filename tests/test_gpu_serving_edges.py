@@ -140,3 +140,37 @@ def test_scores_of_any_size(new, dt, impl, lay, e, sign):
         others = (300 + new) * 12 * math.exp(-0.75 * 2.0 ** e / math.sqrt(hd))
         tol = v.abs() * (2 * H if dt == BF else 2.0 ** -20) + others
         assert ((out[c.cu[r]:c.cu[r + 1]] - v).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("reqs,lay", [([(2500, 1)] * 64, (32, 8, 128)), ([(3000, 512)] * 8, (16, 8, 128)),
+                                      ([(3000, 512)] * 8, (16, 8, 64)), ([(2500, 1)] * 40 + [(3000, 512)] * 6, (16, 8, 128))])
+def test_expired_wait_is_reported_and_the_next_launch_is_clean(reqs, lay):
+    """With the bound of the waits at one cycle an ordinary launch gives up at a wait for its first copies,
+    says so in the error word and returns; with the default bound the same call is clean and has the
+    same bits as before.  (Single tokens at head_dim 128 only: at 64 the decode-step kernel, the same
+    code, is slower than its copies and may never have to wait.)"""
+    from zeroth_order_fine_b200 import zo
+    Hq, Hkv, hd = lay
+    g = torch.Generator(device="cuda").manual_seed(7)
+    page, R = 16, len(reqs)
+    blocks = max(-(-(a + b) // page) for a, b in reqs)
+    cache = torch.randn(R * blocks * page, 2 * Hkv * hd, generator=g, device="cuda").to(BF)
+    table = torch.randperm(R * blocks, generator=g, device="cuda").to(torch.int32).view(R, blocks)
+    cu = [0]
+    for _, b in reqs:
+        cu.append(cu[-1] + b)
+    q = torch.randn(cu[-1], Hq * hd, generator=g, device="cuda").to(BF)
+    args = (q, cache, table, page, i32(cu), i32([a + b for a, b in reqs]), max(b for _, b in reqs), Hq, Hkv, hd)
+    want = zo.zo_op_attention_paged(*args)
+    assert zo.zo_op_error_word() == 0
+    old = zo.zo_op_set_wait_limit(1)
+    try:
+        zo.zo_op_attention_paged(*args)               # queued: returns
+        assert zo.zo_op_error_word() & 1
+    finally:
+        assert zo.zo_op_set_wait_limit(0) == 1
+    assert old > 10 ** 9
+    assert zo.zo_op_error_word() == 0
+    for _ in range(2):
+        assert torch.equal(zo.zo_op_attention_paged(*args), want)
+        assert zo.zo_op_error_word() == 0

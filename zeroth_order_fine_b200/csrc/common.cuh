@@ -61,6 +61,10 @@ __device__ __forceinline__ float block_max(float v, float* red /* >= 32 floats *
     return warp_max(s);
 }
 
+// A wait's verdict for the whole warp: what follows is done by all lanes together (votes, tensor memory
+// loads, MMAs), so when the bound ends some lanes' waits just as the copy lands, all of them give up.
+__device__ __forceinline__ bool whole_warp(bool there) { return __all_sync(0xffffffffu, there); }
+
 inline unsigned cdiv(long long a, long long b) { return (unsigned)((a + b - 1) / b); }
 
 // Raises a kernel's dynamic shared memory limit, once per device (the attribute belongs to the

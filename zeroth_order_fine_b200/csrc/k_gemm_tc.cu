@@ -2308,6 +2308,7 @@ long long gemm_tc_set_wait_cycles(long long cycles) {
     g_wait_cycles = cycles > 0 ? cycles : WAIT_CYCLES;
     return old;
 }
+long long gemm_tc_wait_cycles() { return g_wait_cycles; }
 
 int gemm_tc_adapters(const AdapterArgs& a, const AdapterTiles& t, cudaStream_t st) {
     const int K2 = a.n_adapters * a.rank;

@@ -49,7 +49,6 @@ constexpr int THREADS = 384;
 constexpr int ATOM = 128 * 128;                      // 64 columns of 128 rows
 constexpr int GROUPS = 1024;
 constexpr int MAX_CTAS = 148;
-constexpr long long WAIT_CYCLES = 4000000000ll;
 constexpr uint32_t DRAIN_POLLS = 1u << 24;
 constexpr uint32_t IDESC_QK = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(UK >> 3) << 17) |
                               ((uint32_t)(128 >> 4) << 24);
@@ -91,6 +90,7 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
     return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((uint32_t)ATOM >> 4) << 16) |
            ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
 }
+// suspends the thread for ~1 us at most, so that a waiting one looks at its clock regularly
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -101,18 +101,21 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// Bounded wait, by itself for each lane; false when the bound ended it or another role gave up.  The bound
+// lies LIMIT_AT ints behind the flag: a register for it would be one too many in the softmax.
+constexpr int LIMIT_AT = 9;
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_f) {
     if (bar_try(bar, parity)) return true;
-    const long long t0 = clock64();
-    for (;;) {
-        if (bar_try(bar, parity)) return true;
+    const long long t0 = clock64(), limit = *reinterpret_cast<volatile long long*>(abort_f + LIMIT_AT);
+    do {
         if (*abort_f) return false;
-        if (clock64() - t0 > WAIT_CYCLES) {
+        if (clock64() - t0 > limit) {
             *abort_f = 1;
             atomicOr(&g_chunk_error, 1);
             return false;
         }
-    }
+    } while (!bar_try(bar, parity));
+    return true;
 }
 __device__ __forceinline__ bool elect_one() {
     uint32_t ok;
@@ -334,6 +337,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     volatile int* abort_f = reinterpret_cast<volatile int*>(tail + 260);
     volatile int* bad_unit = reinterpret_cast<volatile int*>(tail + 264);          // [8]
     Line::Cursor* first = reinterpret_cast<Line::Cursor*>(tail + 304);
+    static_assert((260 + 4 * LIMIT_AT) % 8 == 0 && 260 + 4 * LIMIT_AT + 8 <= 304 && 4 * LIMIT_AT >= 36, "limit");
     static_assert(8 * (2 * STAGES + 11) <= 256 && 304 + sizeof(Line::Cursor) <= G::TAIL, "tail");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -351,6 +355,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         bar_init(drain, 1);
         *abort_f = 0;
+        *reinterpret_cast<volatile long long*>(abort_f + LIMIT_AT) = a.wait_cycles;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     grid_dep_launch();                                // the joining kernel may be scheduled
@@ -410,7 +415,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
                     const int s = loads % STAGES;
-                    if (!wait_bar(empty(s), ((loads / STAGES) & 1) ^ 1u, abort_f)) { ok = false; break; }
+                    if (!whole_warp(wait_bar(empty(s), ((loads / STAGES) & 1) ^ 1u, abort_f))) { ok = false; break; }
                     if (lane == 0) {
                         if (kv == 0) bad_unit[unit & 7] = k.q.bad || have != asked;
                         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full(s)),
@@ -434,7 +439,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer ----------------
-        // the whole warp runs the loop, so that its counters stay uniform; one lane issues
+        // the whole warp runs the loop, so that its counters stay uniform; one lane issues, and no lane
+        // needs another, so each takes its own waits' verdicts
         const bool leader = elect_one();
         {
             const uint64_t dq = desc_k(base), dk = desc_k(ring), dv = desc_mn(ring);
@@ -505,8 +511,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
             }
-            if (issued) {
-                if (leader) commit(drain);            // every MMA retires before TMEM is freed
+            if (leader && issued) {
+                commit(drain);                        // every MMA retires before TMEM is freed
                 drain_bar(drain, 0);
             }
         }
@@ -550,7 +556,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int e = p.end(t);
             const uint64_t c2 = pair(sl2, sl2);
             for (int c = p.c0; c < e; ++c) {
-                if (!wait_bar(s_full(t), ns & 1, abort_f)) { ok = false; break; }
+                const bool there = wait_bar(s_full(t), ns & 1, abort_f);     // (the whole warp's verdict below)
                 ++ns;
                 fence_after();
                 bad |= bad_unit[(unit + c - p.c0) & 7] != 0;
@@ -567,8 +573,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                     // reference has its own, which with scores of 2^31 and more is over 2^7 in the
                     // exponent: no weight left, or none finite.  So the other pass, the one with the masks, takes
                     // the reference off before it scales.
-                    const bool plain = cut >= UK && (fabsf(m) <= 0x1p20f || m == -FLT_MAX);
-                    const bool masked = !__all_sync(0xffffffffu, plain);
+                    const bool plain = there && cut >= UK && (fabsf(m) <= 0x1p20f || m == -FLT_MAX);
+                    const bool masked = !whole_warp(plain);
+                    if (masked && !whole_warp(there)) { ok = false; break; }
                     const uint64_t m2 = pair(-m, -m), r2 = pair(-raw, -raw);
                     uint32_t sv[2][16];
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -625,6 +632,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     m = mn;
                     if (move) raw = most;
                 }
+                if (!ok) break;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) l[i] = ln[i];
                 tmem_st32(ts, pk);
@@ -634,7 +642,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (valid < UK && (valid & 15)) {
                     // the value rows behind the last key, up to the end of its 16-key step
                     const int vt = 2 * (unit + c - p.c0) + 1, vs = vt % STAGES;
-                    if (!wait_bar(full(vs), (vt / STAGES) & 1, abort_f)) { ok = false; break; }
+                    if (!whole_warp(wait_bar(full(vs), (vt / STAGES) & 1, abort_f))) { ok = false; break; }
                     const int rows = 16 - (valid & 15);
                     for (int i = (warp & 3) * 32 + lane; i < rows * (HD / 8); i += 128) {
                         const int vr = valid + i / (HD / 8), ch = i % (HD / 8);
@@ -681,7 +689,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             if (done.any(t)) {
-                if (!wait_bar(pv_done(t), (ns - 1) & 1, abort_f)) { ok = false; break; }
+                if (!whole_warp(wait_bar(pv_done(t), (ns - 1) & 1, abort_f))) { ok = false; break; }
                 fence_after();
                 const float inv = 1.f / lt;
                 __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +

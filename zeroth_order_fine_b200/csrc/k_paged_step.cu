@@ -44,7 +44,6 @@ constexpr int UK = 16;                               // keys per unit
 constexpr int GROUPS = 1024;                         // prefix entries kept in shared memory
 constexpr int MAX_CTAS = 148;
 constexpr int MAX_WORKERS = MAX_CTAS * WARPS;
-constexpr long long WAIT_CYCLES = 4000000000ll;      // ~2 s: a copy that never lands
 constexpr uint32_t DRAIN_POLLS = 1u << 24;
 
 __device__ int g_step_error = 0;                     // bit 0: a bounded wait expired
@@ -60,6 +59,17 @@ struct Geo {
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// suspends the thread for ~1 us at most, so that a waiting one looks at its clock regularly
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -70,17 +80,22 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// one look of a wait: under a bound that is less than a suspension, without one
+__device__ __forceinline__ bool bar_poll(uint32_t bar, uint32_t parity, long long limit) {
+    return limit < 4000 ? bar_test(bar, parity) : bar_try(bar, parity);
+}
 // Bounded wait of a whole warp for a unit's copy.
 __device__ __forceinline__ bool wait_unit(uint32_t bar, uint32_t parity, long long limit) {
-    if (bar_try(bar, parity)) return true;
-    const long long t0 = clock64();
-    for (;;) {
-        if (bar_try(bar, parity)) return true;
-        if (clock64() - t0 > limit) {
-            atomicOr(&g_step_error, 1);
-            return false;
-        }
+    bool there = bar_poll(bar, parity, limit);
+    if (!there) {
+        const long long t0 = clock64();
+        while (!(there = bar_poll(bar, parity, limit)))
+            if (clock64() - t0 > limit) {
+                atomicOr(&g_step_error, 1);
+                break;
+            }
     }
+    return whole_warp(there);
 }
 __device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -335,7 +350,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[mt][nb][e] = 0.f;
         }
-        if (!wait_unit(bar0 + 8u * stage, phase, WAIT_CYCLES)) {
+        if (!wait_unit(bar0 + 8u * stage, phase, a.wait_cycles)) {
             alive = false;
             break;
         }

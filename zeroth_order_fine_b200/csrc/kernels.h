@@ -175,6 +175,7 @@ int gemm_tc_error_word();                           // bit 0: a bounded wait exp
 // Bound of every mbarrier wait in the tensor-core GEMM kernels launched from now on, in
 // clock64 cycles (<= 0: the default, about 2 s); returns the previous bound.
 long long gemm_tc_set_wait_cycles(long long cycles);
+long long gemm_tc_wait_cycles();            // the bound that launches get now
 
 // ---- attention -----------------------------------------------------------------------
 struct AttnArgs {
@@ -225,6 +226,7 @@ struct PagedArgs {
     int line_heads;                         // groups of kv heads on a kernel's line of work
     int step_tokens;                        // requests of at most so many new tokens take the
                                             // decode-step kernel
+    long long wait_cycles;                  // bound of every mbarrier wait (clock64 cycles)
 };
 cudaError_t launch_paged_attention(PagedArgs a, cudaStream_t st);          // CUDA cores
 size_t paged_attention_workspace(int hd);

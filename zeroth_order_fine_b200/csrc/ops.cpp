@@ -371,6 +371,7 @@ int zo_op_attention_paged(const void* q, int64_t ld_q, const void* cache, int64_
     a.dtype = dtype == ZO_DTYPE_BF16 ? E_BF16 : E_F32;
     a.out = out; a.ld_out = ld_out;
     a.ws = ws;
+    a.wait_cycles = gemm_tc_wait_cycles();
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (impl != ZO_IMPL_CUDA_CORES && paged_tc_supported(a)) {
         // Requests of up to 16 query rows per kv head: the decode-step kernel; others: the chunk

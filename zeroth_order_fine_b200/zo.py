@@ -596,8 +596,8 @@ def zo_op_rope_table(max_pos: int, head_dim: int, theta: float, device="cuda"):
 
 
 def zo_op_set_wait_limit(cycles: int) -> int:
-    """Bound of every mbarrier wait in the tensor-core GEMMs (<= 0: the default); returns
-    the previous bound."""
+    """Bound of every mbarrier wait in the tensor-core GEMMs and the paged attention's tensor-core
+    kernels (<= 0: the default); returns the previous bound."""
     return int(lib().zo_op_set_wait_limit(cycles))
 
 
