@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int t = blockIdx.x; t < n_items; t += gridDim.x) {
             int mb, nb;
             tile_coords(t / ks, p, &mb, &nb);
-            if (!mbar_wait(tfull(acc), aph, abort_f, p.err, p.wait_cycles)) break;
+            if (!whole_warp(mbar_wait(tfull(acc), aph, abort_f, p.err, p.wait_cycles))) break;
             tc_fence_after();
             const int m = mb * BM + lane_base + lane;
             float run_max = -FLT_MAX, run_sum = 0.f;
@@ -1308,7 +1308,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         for (int t = pair; t < n_items; t += n_pairs) {
             int mb, nb;
             tile_coords2(SPLIT ? t / p.ksplit : t, p, &mb, &nb);
-            if (!mbar_wait(tfull(acc), aph, abort_f, p.err, p.wait_cycles)) break;
+            if (!whole_warp(mbar_wait(tfull(acc), aph, abort_f, p.err, p.wait_cycles))) break;
             tc_fence_after();
             const int m_base = mb * BM2 + (int)rank * 128 + lane_base;
             epilogue_tma<EPI, F8, SPLIT, LIST>(p, &tmC, stg, stg_ptr, buf, m_base, nb,
@@ -1574,7 +1574,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         uint32_t tph = 0;
         int i = 0;
         for (int t = pair; t < n_tiles; t += n_pairs, ++i) {
-            if (!mbar_wait(tfull, tph, abort_f, p.err, p.wait_cycles)) break;
+            if (!whole_warp(mbar_wait(tfull, tph, abort_f, p.err, p.wait_cycles))) break;
             tc_fence_after();
             int tile = t, blk[2] = {0, -1};
             if constexpr (LIST) list_item(t, &tile, blk);
@@ -1582,8 +1582,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             bool ok = true;
             if (rank == 1) {
                 // the previous tile's half has been read before this one overwrites it
-                if (i > 0 && !mbar_wait_cluster(part_free, (uint32_t)((i - 1) & 1), abort_f, p.err,
-                                                p.wait_cycles))
+                if (i > 0 && !whole_warp(mbar_wait_cluster(part_free, (uint32_t)((i - 1) & 1), abort_f, p.err,
+                                                           p.wait_cycles)))
                     ok = false;
                 if (ok) {
                     for (int c = 0; c < BNT / 32; ++c) {
@@ -1603,7 +1603,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                     if (lane == 0) mbar_arrive_cluster(peer_full);
                 }
             } else {
-                if (!mbar_wait_cluster(part_full, (uint32_t)(i & 1), abort_f, p.err, p.wait_cycles))
+                if (!whole_warp(mbar_wait_cluster(part_full, (uint32_t)(i & 1), abort_f, p.err, p.wait_cycles)))
                     ok = false;
                 if (ok) {
                     const float* pr = part + (size_t)r * TS::PART_LD;
