@@ -12,7 +12,7 @@ import pytest
 import torch
 
 from gpu_util import needs_gpu
-from test_gpu_serving import BF, FP, H, U, Paged, i32
+from test_gpu_serving import BF, FP, H, U, Paged, adapt_case, adapt_ref, i32, spans
 
 pytestmark = [pytest.mark.gpu, needs_gpu]
 
@@ -174,3 +174,57 @@ def test_expired_wait_is_reported_and_the_next_launch_is_clean(reqs, lay):
     for _ in range(2):
         assert torch.equal(zo.zo_op_attention_paged(*args), want)
         assert zo.zo_op_error_word() == 0
+
+
+# ---- adapters -----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dt,impl", [(BF, 0), (BF, 1), (FP, 1)])
+@pytest.mark.parametrize("M,N,K", [(2, 264, 128), (48, 1000, 328), (300, 264, 200), (700, 1032, 264), (1100, 520, 64)])
+@pytest.mark.parametrize("form", ["store", "relu", "accumulate"])
+def test_a_row_that_is_not_finite_leaves_the_others_their_bits(M, N, K, form, dt, impl):
+    """NaN and infinity in two rows of x, an id that names no adapter, an infinite factor: these rows are as
+    the definition has them, every other element has the bits of the call without them."""
+    from zeroth_order_fine_b200 import zo
+    n, r = 6, 16
+    ids = spans(M, n, M, 1, 9)
+    x, W, A, B, idt, sc, b = adapt_case(M, N, K, n, r, ids, dt, seed=M)
+    y0 = torch.randn(M, N, generator=torch.Generator().manual_seed(1))
+
+    def call(x, B, idt):
+        y = y0.cuda().clone() if form == "accumulate" else None
+        return zo.zo_op_linear_adapters(x.cuda(), W.cuda(), A.cuda(), B.cuda(), idt.cuda(), sc.cuda(), bias=b.cuda(),
+                                        act=int(form == "relu"), accumulate=form == "accumulate", out=y, impl=impl)
+
+    clean = call(x, B, idt)
+    _, tol = adapt_ref(x, W, A, B, idt, sc, b, n, r, dt == BF and form != "accumulate", dt == BF and impl != 1)
+    tol += 2 * U * (tol + y0.abs().double() + 40) if form == "accumulate" else 0.0    # |y| < 40
+    for kind in ("rows", "id", "factor"):
+        x2, B2, id2 = x.clone(), B.clone(), idt.clone()
+        touched = torch.zeros(M, N, dtype=torch.bool)
+        if kind == "rows":
+            x2[M // 2, 3], x2[0, 5] = NAN, INF
+            touched[[0, M // 2]] = True
+        elif kind == "id":
+            id2[M // 3] = n
+            touched[M // 3] = True
+        else:
+            B2[N // 2, 2 * r + 3] = -INF
+            touched[:, N // 2] = True                 # (another form of the same element's sum)
+        y = call(x2, B2, id2).cpu()
+        assert torch.equal(y[~touched], clean.cpu()[~touched]), kind
+        ref = x2.double() @ W.double().T + b.double()
+        for m in range(M):
+            a = int(id2[m])
+            if 0 <= a < n:
+                ref[m] += B2[:, a * r:(a + 1) * r].double() @ (sc[a].double() * (A[a * r:(a + 1) * r].double() @ x2[m].double()))
+            elif a != -1:
+                ref[m] = NAN
+        if form == "relu":
+            ref = torch.where(ref < 0, torch.zeros((), dtype=torch.float64), ref)
+        elif form == "accumulate":
+            ref += y0.double()
+        odd = ~ref.isfinite()
+        assert torch.equal(y.isnan(), ref.isnan()), kind
+        assert torch.equal(y[odd & ~ref.isnan()].double(), ref[odd & ~ref.isnan()]), kind
+        assert ((y.double() - ref).abs() <= tol)[~odd].all(), kind
+    assert zo.zo_op_error_word() == 0

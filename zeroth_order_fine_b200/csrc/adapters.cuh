@@ -24,6 +24,7 @@ __device__ inline float adapter_element(const AdapterArgs& a, const __nv_bfloat1
     const uint4* x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + (size_t)m * a.K);
     const uint4* w = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.W) + (size_t)n * a.K);
     float v = 0.f;
+#pragma unroll 4
     for (int k = lane; k < a.K / 8; k += lanes) {
         float xv[8], wv[8];
         bf8(__ldg(x + k), xv);

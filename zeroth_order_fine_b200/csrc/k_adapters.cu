@@ -660,38 +660,92 @@ __global__ void __launch_bounds__(256)
     if (tid == 0) cnt[blockIdx.x] = base;
 }
 
-// Chunks of 32 rows x 32 columns that the product's epilogue marked, and rows whose id names no
-// adapter: marked chunks are computed anew from the rows' own factors, one warp per output, and
-// rows without an adapter to name become NaN.  On finite weights nothing is marked and the kernel
-// only reads the marks.
-constexpr int FIX_THREADS = 256;
+// Elements that the product's epilogue named, in the chunks of 32 rows x 32 columns that it marked, and rows
+// whose id names no adapter: the elements are computed anew from the rows' own factors, and rows without an
+// adapter to name become NaN.  On finite weights nothing is marked and the kernel only reads the
+// marks.  A warp takes a chunk, lists its elements and computes 8 at a time, so that 16 loads are in
+// flight (4093 rows, 20480 x 5120, 0.63 ms: one NaN row, all of its outputs, 0.5 ms more; in CTAs of 128
+// chunks instead of 32 4.3 ms more and 2 us less when nothing is marked; whole chunks of 32 rows computed
+// element by element 229 ms more, and with other bits in the 31 rows beside it).
+constexpr int FIX_THREADS = 256, FIX_CHUNKS = 32, FIX_N = 8;
 __global__ void __launch_bounds__(FIX_THREADS)
     adapter_repair_kernel(AdapterArgs a, const __nv_bfloat16* __restrict__ S, int ldS,
-                          const uint8_t* __restrict__ odd) {
+                          const uint8_t* __restrict__ odd, const uint32_t* __restrict__ bits) {
     grid_dep_wait();
+    __shared__ uint16_t elems[FIX_THREADS / 32][1024];           // row << 5 | column
     const int chunks = (a.N + 31) / 32, m0 = blockIdx.x * 32;
+    const int c0 = blockIdx.y * FIX_CHUNKS, c1 = min(chunks, c0 + FIX_CHUNKS);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int id_l = m0 + lane < a.M ? a.ids[m0 + lane] : -1;
     const unsigned none = __ballot_sync(0xffffffffu, id_l < -1 || id_l >= a.n_adapters);
     // usually nothing is marked: all of the CTA's marks in one look
     int any = none != 0u;
-    for (int c = threadIdx.x; c < chunks; c += FIX_THREADS) any |= odd[(size_t)blockIdx.x * chunks + c];
+    for (int c = c0 + (int)threadIdx.x; c < c1; c += FIX_THREADS) any |= odd[(size_t)blockIdx.x * chunks + c];
     if (!__syncthreads_or(any)) return;
-    for (int c = warp; c < chunks; c += FIX_THREADS / 32) {
-        const bool marked = odd[(size_t)blockIdx.x * chunks + c] != 0;
-        if (!marked && !none) continue;
-        for (int r = 0; r < 32 && m0 + r < a.M; ++r) {
-            const int m = m0 + r;
-            const int id = __shfl_sync(0xffffffffu, id_l, r);
-            const bool bad = (none >> r) & 1u;
-            if (!marked && !bad) continue;
-            float mine = __int_as_float(0x7fc00000);
-            if (!bad)
-                for (int j = 0; j < 32 && c * 32 + j < a.N; ++j) {
-                    const float v = warp_sum(adapter_element(a, S, ldS, m, c * 32 + j, id, lane, 32));
-                    if (lane == j) mine = v;
+    for (int c = c0 + warp; c < c1; c += FIX_THREADS / 32) {
+        const int n0 = c * 32;
+        for (unsigned rows = none; rows; rows &= rows - 1)
+            if (n0 + lane < a.N) adapter_store(a, m0 + __ffs(rows) - 1, n0 + lane, __int_as_float(0x7fc00000));
+        if (!odd[(size_t)blockIdx.x * chunks + c]) continue;
+        uint32_t mine = m0 + lane < a.M && !((none >> lane) & 1u) ? bits[(size_t)(m0 + lane) * chunks + c] : 0u;
+        if (a.N - n0 < 32) mine &= (1u << (a.N - n0)) - 1u;
+        int end = __popc(mine);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, end, o);
+            if (lane >= o) end += v;
+        }
+        const int total = __shfl_sync(0xffffffffu, end, 31);
+        __syncwarp();                          // the list before has been read
+        for (int at = end - __popc(mine); mine; mine &= mine - 1) elems[warp][at++] = (uint16_t)(lane << 5 | (__ffs(mine) - 1));
+        __syncwarp();
+        for (int e0 = 0; e0 < total; e0 += FIX_N) {
+            const uint4 *x[FIX_N], *w[FIX_N];
+            const __nv_bfloat16 *s[FIX_N], *f[FIX_N];
+            bool has[FIX_N];
+            float v[FIX_N];
+#pragma unroll
+            for (int i = 0; i < FIX_N; ++i) {
+                const int e = elems[warp][min(e0 + i, total - 1)];
+                x[i] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + (size_t)(m0 + (e >> 5)) * a.K);
+                w[i] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.W) + (size_t)(n0 + (e & 31)) * a.K);
+                v[i] = 0.f;
+            }
+            for (int k = lane; k < a.K / 8; k += 32) {
+                uint4 xu[FIX_N], wu[FIX_N];
+#pragma unroll
+                for (int i = 0; i < FIX_N; ++i) {
+                    xu[i] = __ldg(x[i] + k);
+                    wu[i] = __ldg(w[i] + k);
                 }
-            if (c * 32 + lane < a.N) adapter_store(a, m, c * 32 + lane, mine);
+#pragma unroll
+                for (int i = 0; i < FIX_N; ++i) {
+                    float xv[8], wv[8];
+                    bf8(xu[i], xv);
+                    bf8(wu[i], wv);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v[i] = fmaf(xv[q], wv[q], v[i]);
+                }
+            }
+            // the expand, the row's own factors (rows of a chunk may have several adapters)
+#pragma unroll
+            for (int i = 0; i < FIX_N; ++i) {
+                const int e = elems[warp][min(e0 + i, total - 1)], id = __shfl_sync(0xffffffffu, id_l, e >> 5);
+                s[i] = S + (size_t)(m0 + (e >> 5)) * ldS + (size_t)max(id, 0) * a.rank;
+                f[i] = static_cast<const __nv_bfloat16*>(a.B) + (size_t)(n0 + (e & 31)) * a.n_adapters * a.rank +
+                       (size_t)max(id, 0) * a.rank;
+                has[i] = id >= 0;
+            }
+            for (int k = lane; k < a.rank; k += 32)
+#pragma unroll
+                for (int i = 0; i < FIX_N; ++i)
+                    if (has[i]) v[i] = fmaf(__bfloat162float(s[i][k]), __bfloat162float(f[i][k]), v[i]);
+#pragma unroll
+            for (int i = 0; i < FIX_N; ++i) {
+                const float y = warp_sum(v[i]);
+                const int e = elems[warp][min(e0 + i, total - 1)];
+                if (lane == i && e0 + i < total) adapter_store(a, m0 + (e >> 5), n0 + (e & 31), y);
+            }
         }
     }
 }
@@ -728,7 +782,7 @@ int pass_rows(int M, int K2) {
     return (size_t)M < rows ? M : (int)rows;
 }
 struct TileSpace {
-    size_t list, s, odd, total;           // offsets
+    size_t list, s, odd, bits, total;     // offsets
     int blocks, n_list, ld;
 };
 TileSpace tile_space(int M, int N, int K2) {
@@ -741,7 +795,8 @@ TileSpace tile_space(int M, int N, int K2) {
     t.list = up256((size_t)t.blocks * 4);
     t.s = t.list + up256((size_t)t.blocks * t.n_list * 4);
     t.odd = t.s + up256((size_t)rows * t.ld * 2);
-    t.total = t.odd + up256((size_t)((rows + 31) / 32) * ((N + 31) / 32));
+    t.bits = t.odd + up256((size_t)((rows + 31) / 32) * ((N + 31) / 32));
+    t.total = t.bits + up256((size_t)rows * ((N + 31) / 32) * 4);
     return t;
 }
 
@@ -835,6 +890,7 @@ cudaError_t launch_linear_adapters_tc(const AdapterArgs& a, cudaStream_t st, boo
     at.S = ws + t.s;
     at.ldS = t.ld;
     at.odd = reinterpret_cast<uint8_t*>(ws + t.odd);
+    at.bits = reinterpret_cast<uint32_t*>(ws + t.bits);
     if (step_form(a.M, a.N, a.K, K2, a.rank)) {
         GemmArgs g;
         memset(&g, 0, sizeof(g));
@@ -866,8 +922,9 @@ cudaError_t launch_linear_adapters_tc(const AdapterArgs& a, cudaStream_t st, boo
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         if (gemm_tc_adapters(b, at, st)) return cudaErrorUnknown;
-        e = launch_pdl(adapter_repair_kernel, dim3(cdiv(b.M, 32)), dim3(FIX_THREADS), 0, st, b,
-                       static_cast<const __nv_bfloat16*>(at.S), at.ldS, static_cast<const uint8_t*>(at.odd));
+        e = launch_pdl(adapter_repair_kernel, dim3(cdiv(b.M, 32), cdiv(cdiv(b.N, 32), FIX_CHUNKS)),
+                       dim3(FIX_THREADS), 0, st, b, static_cast<const __nv_bfloat16*>(at.S), at.ldS,
+                       static_cast<const uint8_t*>(at.odd), static_cast<const uint32_t*>(at.bits));
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -104,9 +104,9 @@ struct TcParams {
     int dep_late;                           // EPI_SPLIT_T: wait for the kernel before at the end
     // adapters (LIST kernels): row block mb takes cnt[mb] extension blocks, list[mb * n_list + i]
     // = block | mask of its 16-column steps << 16; odd[m / 32][n / 32]: a chunk whose accumulators
-    // are not all finite (left to the repair kernel)
+    // are not all finite, then bits[m][n / 32] names those that are not (the repair kernel's work)
     const int* cnt; const int* list; int n_list;
-    uint8_t* odd;
+    uint8_t* odd; uint32_t* bits;
     // the adapters' shrink: row ids, scales, rank
     const int* ids; const float* ad_scale; int n_adapters, ad_rank;
     // decode steps under adapters: one split, so the kernel writes the output itself
@@ -620,9 +620,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
                                 for (int q = 0; q < 32; ++q)
                                     if (q == j) y = v[q];
+                                // a few such features (a factor of another adapter): one by one by the
+                                // warp; many (the token's own row): each by its lane
+                                const bool anew = m < p.M && !((odd_ids >> j) & 1u) && !isfinite(y);
+                                const unsigned all = __ballot_sync(0xffffffffu, anew);
+                                if (__popc(all) > 8) {
+                                    if (anew) y = adapter_element(p.ad, p.ad_S, p.ad_ldS, n + j, m, id, 0, 1);
+                                } else {
+                                    for (unsigned b = all; b; b &= b - 1) {
+                                        const int l = __ffs(b) - 1;
+                                        const float t = warp_sum(adapter_element(p.ad, p.ad_S, p.ad_ldS, n + j,
+                                                                                 m - lane + l, id, lane, 32));
+                                        if (lane == l) y = t;
+                                    }
+                                }
                                 if ((odd_ids >> j) & 1u) y = __int_as_float(0x7fc00000);
-                                else if (m < p.M && !isfinite(y))
-                                    y = adapter_element(p.ad, p.ad_S, p.ad_ldS, n + j, m, id, 0, 1);
                                 if (m < p.M) adapter_store(p.ad, n + j, m, y);
                             }
                         } else if (m < p.M) {
@@ -858,18 +870,27 @@ __device__ __forceinline__ void dequant_chunk(const TcParams& p, int m, int n, f
 //
 // LIST (adapters): a row's extension columns of other adapters are 0, and 0 times a non-finite
 // expand factor would not be 0.  So a chunk of 32 columns with an accumulator that is not finite
-// is not stored but marked, and the repair kernel computes it from the rows' own factors.
+// is marked, and the repair kernel computes these elements, and no others, from the rows' own factors.
 template <int EPI, bool F8, bool SPLIT, bool LIST>
 __device__ __forceinline__ void epilogue_tma(const TcParams& p, const CUtensorMap* tmC,
                                              uint32_t stg, uint8_t* stg_ptr, int& buf, int m_base,
                                              int nb, uint32_t taddr, int lane, int split) {
     const int r = lane;
-    // marks the 32-column chunks from column n (z: the sum of 0 times the thread's accumulators,
-    // NaN if one is not finite); true: not to be stored
-    auto is_odd = [&](float z, int n, int chunks) {
+    // marks the 32-column chunks from column n (z: the sum of 0 times the thread's accumulators v,
+    // NaN if one is not finite), and names the elements of marked ones
+    auto is_odd = [&](float z, int n, int chunks, const float* v) {
         const bool odd = __any_sync(0xffffffffu, z != 0.f);
         if (lane < chunks && n + 32 * lane < p.N && m_base < p.M)
             p.odd[(size_t)(m_base >> 5) * ((p.N + 31) >> 5) + (n >> 5) + lane] = odd;
+        if (odd && m_base + r < p.M)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                if (c < chunks && n + 32 * c < p.N) {
+                    uint32_t b = 0;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) b |= isfinite(v[32 * c + j]) ? 0u : 1u << j;
+                    p.bits[(size_t)(m_base + r) * ((p.N + 31) >> 5) + (n >> 5) + c] = b;
+                }
         return odd;
     };
     auto stage_begin = [&]() {
@@ -914,8 +935,12 @@ __device__ __forceinline__ void epilogue_tma(const TcParams& p, const CUtensorMa
             if (n >= p.N) break;
             float v[32];
             tmem_ld32(taddr + (uint32_t)(c * 32), v);
-            if (LIST && is_odd(zero_times<32>(v), n, 1)) continue;
-            if (p.bias) {
+            if (LIST && is_odd(zero_times<32>(v), n, 1, v)) {
+                // nothing is added to the elements left to the repair
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    v[j] = !isfinite(v[j]) ? -0.f : p.bias && n + j < p.N ? v[j] + __ldg(p.bias + n + j) : v[j];
+            } else if (p.bias) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] += (n + j < p.N) ? __ldg(p.bias + n + j) : 0.f;
             }
@@ -1055,7 +1080,7 @@ __device__ __forceinline__ void epilogue_tma(const TcParams& p, const CUtensorMa
             tmem_ld32(taddr + (uint32_t)(c * 32), y);
             tmem_ld32(taddr + (uint32_t)((c + 1) * 32), y + 32);
             if (F8) dequant_chunk<64>(p, m_base + r, n, y);
-            if (LIST && is_odd(zero_times<64>(y), n, 2)) continue;
+            if (LIST) is_odd(zero_times<64>(y), n, 2, y);      // (the repair stores over the odd ones)
 #pragma unroll
             for (int j = 0; j < 64; ++j) {
                 float v = y[j];
@@ -2347,6 +2372,7 @@ int gemm_tc_adapters(const AdapterArgs& a, const AdapterTiles& t, cudaStream_t s
     p.bias = a.bias;
     p.C = a.y; p.ldc = a.N; p.c_type = a.accumulate ? E_F32 : E_BF16;
     p.odd = t.odd;
+    p.bits = t.bits;
     if (a.accumulate) return launch_epi2<EPI_RESID, false, false, true>(x, w, s2, b2, c, p, st);
     return a.act ? launch_epi2<EPI_STORE_RELU, false, false, true>(x, w, s2, b2, c, p, st)
                  : launch_epi2<EPI_STORE, false, false, true>(x, w, s2, b2, c, p, st);

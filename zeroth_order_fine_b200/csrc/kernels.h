@@ -115,9 +115,9 @@ struct AdapterArgs {
 };
 
 // Row blocks (of 256 rows; of 128 in the decode form): the 64-column blocks of the factors that
-// their rows' adapters touch (cnt, list: see TcParams), the masked shrink S [M x ldS] bf16 and the
-// marks of chunks to repair.
-struct AdapterTiles { const int* cnt; const int* list; int n_list; void* S; int ldS; uint8_t* odd; };
+// their rows' adapters touch (cnt, list: see TcParams), the masked shrink S [M x ldS] bf16, the marks of
+// chunks with elements to repair and those elements (odd, bits: see TcParams).
+struct AdapterTiles { const int* cnt; const int* list; int n_list; void* S; int ldS; uint8_t* odd; uint32_t* bits; };
 
 struct GemmArgs {
     const void* A; int lda; int a_type;     // [M x K], K contiguous
