@@ -228,3 +228,22 @@ def test_a_row_that_is_not_finite_leaves_the_others_their_bits(M, N, K, form, dt
         assert torch.equal(y[odd & ~ref.isnan()].double(), ref[odd & ~ref.isnan()]), kind
         assert ((y.double() - ref).abs() <= tol)[~odd].all(), kind
     assert zo.zo_op_error_word() == 0
+
+
+@pytest.mark.parametrize("M,N,K,r", [(5000, 16384, 8, 4), (4161, 16448, 12, 40)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_fp32_adapters_in_several_passes(M, N, K, r, accumulate):
+    """Outputs past 256 MB: rows in passes, each with its own slices; every row against float64."""
+    from zeroth_order_fine_b200 import zo
+    n = 3
+    c = adapt_case(M, N, K, n, r, spans(M, n, 3, 1, 700), FP, seed=K)
+    d = [t.cuda() for t in c]
+    y0 = torch.randn(M, N, device="cuda") if accumulate else None
+    y = zo.zo_op_linear_adapters(*d[:6], bias=d[6], accumulate=accumulate, out=y0.clone() if accumulate else None)
+    for m0 in range(0, M, 1000):
+        rows = slice(m0, m0 + 1000)
+        ref, tol = adapt_ref(d[0][rows], *d[1:4], d[4][rows], d[5], d[6], n, r, False, False)
+        if accumulate:
+            ref += y0[rows]
+            tol += 2 * U * (ref.abs() + y0[rows].double().abs())
+        assert ((y[rows].double() - ref).abs() <= tol).all(), m0

@@ -281,8 +281,12 @@ __global__ void __launch_bounds__(128)
     }
 }
 
-// K splits of the fp32 product: the fewest whose last round of SMs is full enough (each costs a slice):
-// 301 x 2048 x 2048 under 5 adapters takes 133 us unsplit, 103 in 2, 88 in 4 and 84 in 8.
+// K splits of the fp32 product: the fewest whose last round of SMs is full enough.  301 x 2048 x 2048 under
+// 5 adapters (160 tiles) takes 133 us unsplit, 103 in 2, 88 in 4 and 84 in 8.  Each split costs a slice,
+// written and read: a fiftieth of a round there, and in proportion to the tiles and against K where
+// that is more, so that many full rounds are not split for the last one (2048 x 8192 x 2048: 1.59 ms, 1.62
+// in 4; 4093 x 20480 x 5120: 19.8, 20.2 in 5); 64 MB of slices at most, as in the decode form.
+constexpr size_t SLICES_MOST = (size_t)64 << 20;
 int f32_splits(int M, int N, int K) {
     const long long tiles = (long long)((M + FM - 1) / FM) * ((N + FM - 1) / FM);
     const int blocks = (K + FK - 1) / FK;
@@ -291,13 +295,28 @@ int f32_splits(int M, int N, int K) {
     for (int k = 1; k <= 8 && k <= (blocks + 3) / 4; ++k) {
         const int per = (blocks + k - 1) / k;
         if ((blocks + per - 1) / per != k) continue;
-        const double cost = (double)((tiles * k + 147) / 148) * per / blocks + 0.02 * k;
+        if (k > 1 && (size_t)M * N * k * 4 > SLICES_MOST) break;
+        const double slice = 0.256 * (double)tiles / K;
+        const double cost = (double)((tiles * k + 147) / 148) * per / blocks + (slice > 0.02 ? slice : 0.02) * k;
         if (cost < least) {
             least = cost;
             best = k;
         }
     }
     return best;
+}
+
+// Rows of one pass of the fp32 form: a pass's slice stays within 256 MB, in whole tiles.
+int f32_pass_rows(int M, int N) {
+    size_t rows = ((size_t)256 << 20) / 4 / N / FM * FM;
+    if (rows < FM) rows = FM;
+    return (size_t)M < rows ? M : (int)rows;
+}
+size_t f32_slice_floats(int M, int N, int K) {
+    const int rows = f32_pass_rows(M, N), last = M % rows;
+    const size_t a = (size_t)f32_splits(rows, N, K) * rows * N;
+    const size_t b = last ? (size_t)f32_splits(last, N, K) * last * N : 0;
+    return a > b ? a : b;
 }
 
 // ---- tensor-core forms ----------------------------------------------------------------------
@@ -770,7 +789,7 @@ bool step_form(int M, int N, int K, int K2, int rank) {
 // Slices of the decode form: room for up to 16 splits, 64 MB at most unless one slice is more.
 size_t slice_floats(int M, int N) {
     const size_t one = (size_t)M * N;
-    const size_t most = ((size_t)64 << 20) / 4 / one;
+    const size_t most = SLICES_MOST / 4 / one;
     return one * (most < 1 ? 1 : most > 16 ? 16 : most);
 }
 
@@ -805,7 +824,7 @@ TileSpace tile_space(int M, int N, int K2) {
 size_t adapter_workspace(int M, int N, int K, int n_adapters, int rank, int dtype) {
     const size_t s = up256((size_t)M * rank * 4) + 256;
     if (M == 0) return s;
-    if (dtype != E_BF16) return s + up256((size_t)f32_splits(M, N, K) * M * N * 4);
+    if (dtype != E_BF16) return s + up256(f32_slice_floats(M, N, K) * 4);
     size_t t = tile_space(M, N, n_adapters * rank).total;
     if (step_form(M, N, K, n_adapters * rank, rank)) t += up256(slice_floats(M, N) * 4);
     return t > s ? t : s;
@@ -830,30 +849,43 @@ cudaError_t launch_linear_adapters_simt(const AdapterArgs& a, cudaStream_t st) {
                : a.M == 2 ? launch_rows<float, 2>(a, st)
                : a.M <= 4 ? launch_rows<float, 4>(a, st)
                           : launch_rows<float, 8>(a, st);
-    cudaError_t e = rows16 ? launch_shrink<true>(a, S, st) : launch_shrink<false>(a, S, st);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
     if (rows16) {
         static std::atomic<uint64_t> attr{0};
         e = smem_limit(reinterpret_cast<const void*>(gemm_f32_kernel), F_SMEM, attr);
         if (e != cudaSuccess) return e;
         float* slices = reinterpret_cast<float*>(static_cast<char*>(a.ws) + up256((size_t)a.M * a.rank * 4));
-        const int ks = f32_splits(a.M, a.N, a.K);
-        // The product beside the shrink, unless the shrink is long: then the two fight for L1 and the
-        // shrink reads x again and again from L2 (301 rows, 1544 x 1000: rank 8 45 us beside and 48
-        // behind, rank 64 100 and 66; 2048 x 2048, rank 32: 84 and 88, with adapters changing from row to
-        // row 107 and 103).
-        const dim3 grid(cdiv(a.N, FM), cdiv(a.M, FM), ks);
-        const float *x = static_cast<const float*>(a.x), *W = static_cast<const float*>(a.W);
-        if (a.N >= 64 * a.rank) {
-            e = launch_pdl(gemm_f32_kernel, grid, dim3(F_THREADS), F_SMEM, st, x, W, a.M, a.N, a.K, ks, slices);
-        } else {
-            gemm_f32_kernel<<<grid, F_THREADS, F_SMEM, st>>>(x, W, a.M, a.N, a.K, ks, slices);
-            e = cudaGetLastError();
+        const int rows = f32_pass_rows(a.M, a.N);
+        for (int m0 = 0; m0 < a.M; m0 += rows) {
+            AdapterArgs b = a;
+            b.M = a.M - m0 < rows ? a.M - m0 : rows;
+            b.x = static_cast<const float*>(a.x) + (size_t)m0 * a.K;
+            b.ids = a.ids + m0;
+            b.y = static_cast<float*>(a.y) + (size_t)m0 * a.N;
+            e = launch_shrink<true>(b, S, st);
+            if (e != cudaSuccess) return e;
+            const int ks = f32_splits(b.M, a.N, a.K);
+            // The product beside the shrink, unless the shrink is long: then the two fight for L1 and the
+            // shrink reads x again and again from L2 (301 rows, 1544 x 1000: rank 8 45 us beside and 48
+            // behind, rank 64 100 and 66; 2048 x 2048, rank 32: 84 and 88, with adapters changing from row to
+            // row 107 and 103).
+            const dim3 grid(cdiv(a.N, FM), cdiv(b.M, FM), ks);
+            const float *x = static_cast<const float*>(b.x), *W = static_cast<const float*>(a.W);
+            if (a.N >= 64 * a.rank) {
+                e = launch_pdl(gemm_f32_kernel, grid, dim3(F_THREADS), F_SMEM, st, x, W, b.M, a.N, a.K, ks, slices);
+            } else {
+                gemm_f32_kernel<<<grid, F_THREADS, F_SMEM, st>>>(x, W, b.M, a.N, a.K, ks, slices);
+                e = cudaGetLastError();
+            }
+            if (e != cudaSuccess) return e;
+            e = launch_pdl(adapter_expand_f32_kernel, dim3(cdiv(b.M, ER), cdiv(a.N, 128)), dim3(128), 0, st, b,
+                           static_cast<const float*>(S), static_cast<const float*>(slices), ks);
+            if (e != cudaSuccess) return e;
         }
-        if (e != cudaSuccess) return e;
-        return launch_pdl(adapter_expand_f32_kernel, dim3(cdiv(a.M, ER), cdiv(a.N, 128)), dim3(128), 0, st, a,
-                          static_cast<const float*>(S), static_cast<const float*>(slices), ks);
+        return cudaSuccess;
     }
+    e = launch_shrink<false>(a, S, st);
+    if (e != cudaSuccess) return e;
     adapter_gemm_kernel<<<dim3(cdiv(a.N, BN), cdiv(a.M, BM)), 256, 0, st>>>(a, S);
     return cudaGetLastError();
 }
