@@ -275,10 +275,15 @@ int zo_op_kv_write(const void* qkv, int64_t ld_qkv, const int32_t* slot_map, int
  *   impl     ZO_IMPL_TENSOR_CORES needs bf16, head_dim 64 or 128, at most 128 query heads per
  *            kv head, 16-byte aligned pointers and strides that are multiples of 8 elements;
  *            AUTO picks it then, else CUDA cores
- * A request whose lens is below its new tokens or above max_blocks * page_size or 2^31 - 256, or
- * that names a page outside [0, n_slots / page_size) within its length, gets NaN rows; one whose rows are
- * not inside [0, n_tokens) is left out.  A non-finite key or value can make every row of its
- * own request NaN, also rows before it.
+ * A request whose lens is below its new tokens or above max_blocks * page_size or 2^31 - 256
+ * gets NaN rows; one whose rows are not inside [0, n_tokens) is left out.  Of a request that
+ * names a page outside [0, n_slots / page_size) within its length, the rows that see the page
+ * are NaN, and rows before them are right or NaN (a kernel's tile of rows has one fate).
+ * Contents: a row that sees a NaN score or one of +infinity is NaN, a score of -infinity has no
+ * weight, and with no other a row is NaN.  A non-finite value reaches its column of the rows
+ * that see it, and may make that column of rows before them in the same request NaN.
+ * A row's last bits depend on its batch, unlike zo_op_linear_ext's: keys are cut where the
+ * work of the whole batch is, and max_new picks the kernel.  The same call gives the same bits.
  * ZO_ERR_ARG on NULL pointers, sizes below 1 (n_rows, n_tokens: below 0), n_heads not a
  * multiple of n_kv_heads, strides below the row, a page_size that is no power of two from 8
  * to 256, n_slots no multiple of page_size or above 2^31 - 1, or a workspace too small;

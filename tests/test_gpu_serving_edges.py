@@ -247,3 +247,73 @@ def test_fp32_adapters_in_several_passes(M, N, K, r, accumulate):
             ref += y0[rows]
             tol += 2 * U * (ref.abs() + y0[rows].double().abs())
         assert ((y[rows].double() - ref).abs() <= tol).all(), m0
+
+
+@pytest.mark.parametrize("dt,impl,hint", [(BF, 0, 1000), (BF, 0, 1), (BF, 1, 1000), (FP, 1, 1000)])
+@pytest.mark.parametrize("lay", [(8, 2, 128), (4, 4, 64)])
+@pytest.mark.parametrize("page", [2 ** 31 - 1, -1])
+def test_a_bad_page_behind_the_first_tiles(dt, impl, hint, lay, page):
+    """Rows that see a page outside the pool are NaN; rows of the same request before it are right or NaN,
+    other requests' rows right."""
+    c = Paged([(3, 1), (0, 700), (20, 30)], *lay, 16, dt)
+    c.table[1][40] = page
+    out = c.run(impl, max_new=hint)
+    kv2 = lay[1] * lay[2]
+    c.kv[1][640:656, :kv2] = NAN                      # (the oracle's rows that see it: NaN)
+    no = torch.zeros(700, dtype=torch.bool)
+    n_nan = compare(c, out, impl, may_be_nan=[no[:1], ~no, no[:30]])
+    assert n_nan == 60 * lay[0] * lay[2]
+    assert out[1:1 + 128].isfinite().all()            # a tile that is done by then is not held back
+
+
+COLD = """
+import sys, torch
+sys.path.insert(0, {root!r})
+from zeroth_order_fine_b200 import zo
+BF, FP, dev = torch.bfloat16, torch.float32, "cuda"
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)
+g = torch.Generator(device=dev).manual_seed(1)
+rnd = lambda *s: torch.randn(*s, generator=g, device=dev)
+calls, outs = [], []
+for hd, dt, new in ((128, BF, 1), (128, BF, 100), (64, BF, 1), (64, BF, 100), (64, FP, 3)):
+    q, cache, table = rnd(2 * new, 4 * hd).to(dt), rnd(64 * 16, 4 * hd).to(dt), i32([list(range(32)), list(range(32, 64))])
+    out, ws = torch.zeros(2 * new, 4 * hd, dtype=dt, device=dev), torch.empty(
+        zo.zo_op_attention_paged_workspace(2 * new, 2, 4, 2, hd, dt), dtype=torch.uint8, device=dev)
+    a = (q, cache, table, 16, i32([0, new, 2 * new]), i32([300, 400]), new, 4, 2, hd)
+    calls.append(lambda a=a, out=out, ws=ws: zo.zo_op_attention_paged(*a, out=out, ws=ws)); outs.append(out)
+for M, dt in ((1, BF), (2, BF), (40, BF), (400, BF), (3, FP), (300, FP)):
+    N, K, n, r = 1024, 512, 4, 16
+    a = (rnd(M, K).to(dt), rnd(N, K).to(dt), rnd(n * r, K).to(dt), rnd(N, n * r).to(dt), i32([m % 5 - 1 for m in range(M)]),
+         rnd(n))
+    out, ws = torch.zeros(M, N, dtype=dt, device=dev), torch.empty(
+        zo.zo_op_linear_adapters_workspace(M, N, K, n, r, dt), dtype=torch.uint8, device=dev)
+    calls.append(lambda a=a, out=out, ws=ws: zo.zo_op_linear_adapters(*a, out=out, ws=ws)); outs.append(out)
+ring, s = zo.zo_page_ring(64)
+t, s2, cu, sl = i32([[0] * 8] * 2), i32([0] * 4), i32([0] * 3), i32([0] * 50)
+o, nw, qkv, pool = i32([0, 0]), i32([17, 30]), rnd(50, 4 * 64), rnd(64 * 16, 2 * 64)
+calls.append(lambda: zo.zo_op_block_tables(o, nw, t, ring, s, s2, 16, cu_new=cu, slot_map=sl))
+calls.append(lambda: zo.zo_op_kv_write(qkv, sl, pool, 2, 1, 64))
+outs += [t, s2, cu, sl, pool]
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    for f in calls:
+        f()
+graph.replay()
+torch.cuda.synchronize()
+got = [x.clone() for x in outs]
+for f in calls:
+    f()
+assert zo.zo_op_error_word() == 0
+assert all(torch.equal(a, b) for a, b in zip(got, outs)) and all(x.float().isfinite().all() and x.any() for x in outs)
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Every op captured before it ever ran: the replay gives the bits of the calls."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", COLD.format(root=root)], capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0 and "same" in p.stdout, p.stderr[-3000:]

@@ -19,7 +19,8 @@
 //                the 512 columns with S_A S_B O_A O_B), so S_t of the next unit waits for P_t V
 // The running reference m of a row moves only when its maximum grows by more than 2^8: sums and
 // outputs stay exact in fp32 (P up to 2^8, the same relative rounding) and O is rarely rescaled.
-// Keys a row may not see get probability exactly 0.  Value rows behind the item's last key (the
+// Keys a row may not see get probability exactly 0.  A row whose scores have a NaN or +infinity is NaN (seen
+// by the maximum: the exponentials on the FMA pipe would hide it).  Value rows behind the item's last key (the
 // rest of a page, or what an earlier tile left) are not multiplied: the product takes the 16-key
 // steps that hold keys, and the rest of the last step is cleared in shared memory.
 // Every wait is bounded; on expiry the kernel records the error word, lets what it issued land,
