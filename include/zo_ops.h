@@ -312,6 +312,11 @@ int zo_op_attention_paged(const void* q, int64_t ld_q, const void* cache, int64_
  *        be shared by calls that may run at the same time
  *   impl ZO_IMPL_TENSOR_CORES needs dtype bf16, K, N and n_adapters * rank multiples of 8 and
  *        16-byte aligned pointers; AUTO picks it then for three rows and more, else CUDA cores
+ *        (in bf16 the slow way for many rows: pad a rank of 4 to 8)
+ * A row's last bits depend on its batch, unlike zo_op_linear_ext's: M picks the kernel and the
+ * splits of K, and in bf16 the shrink x A^T is rounded to bf16 from three rows on.  The same call
+ * gives the same bits, and a row that is not finite leaves the others theirs.  There is no q/k
+ * norm, rotary or SwiGLU epilogue: Qwen3's q|k|v and gate|up projections are not this call alone.
  * M = 0 is a no-op.  ZO_ERR_ARG on NULL pointers, negative or empty sizes, rank above 256 or
  * n_adapters * rank above 65536, an unknown act, or a workspace too small or not aligned;
  * ZO_ERR_UNSUPPORTED for M above 4194240. */

@@ -317,3 +317,43 @@ def test_first_calls_of_a_process_inside_a_capture():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     p = subprocess.run([sys.executable, "-c", COLD.format(root=root)], capture_output=True, text=True, timeout=300)
     assert p.returncode == 0 and "same" in p.stdout, p.stderr[-3000:]
+
+
+@pytest.mark.parametrize("new", [1, 200])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("delta", [1e-5, 1e-4])
+def test_the_exponentials_of_a_row_agree_however_they_are_computed(new, hd, delta):
+    """The rounding of p to bf16 hides an exponential's error, unless p lies next to a rounding border.  Here
+    it does: 16 keys in a row share a score whose weight is delta (relative) beside the middle of two
+    bf16 numbers, now on one side, now on the other, and their values are 3 at four of the 16 places
+    and -1 at twelve, four places taken in turn.  The sum is 0 exactly if all 16 weights round alike, so every
+    exponential is right to delta: 2.7e-6 of the chunk kernel's polynomial, 2^-22 of the other, 3 2^-24 * 3 of
+    the scores are below it.  (Weights are 2^-3 to 1, multiples of 2^-11, and sums stay below 2^10: no sum
+    is rounded.)"""
+    heads, ctx = 8, 512
+    c2 = float(torch.tensor(1 / math.sqrt(hd), dtype=FP) * torch.tensor(1.4426950408889634, dtype=FP))
+    c = Paged([(ctx, new)], heads, heads, hd, 16, BF)
+    g = torch.Generator().manual_seed(hd)
+    kv = c.kv[0].view(ctx + new, 2, heads, hd)
+    kv.zero_()
+    kv[ctx:, 0, :, 0] = -400.0                        # the new tokens: next to no weight, value 0
+    for h in range(heads):
+        for group in range(ctx // 16):
+            s = 0.0                                   # in every 128 keys one group at the maximum
+            if group % 8 != h % 8:
+                mid = (1 + (2 * int(torch.randint(128, (), generator=g)) + 1) / 256) * 2.0 ** -int(
+                    torch.randint(1, 4, (), generator=g))
+                s = math.log2(mid * (1 + delta * (1 if group % 2 else -1))) / c2
+            for d in range(3):                        # the score as a sum of three bf16 numbers
+                part = torch.tensor(s).to(BF)
+                kv[group * 16:group * 16 + 16, 0, h, d] = part
+                s -= part.item()
+        at = torch.arange(ctx)
+        for d in range(4):
+            kv[:ctx, 1, h, d] = torch.where(at % 16 // 4 == d, 3.0, -1.0).to(BF)
+    for i in range(ctx + new):
+        c.cache[c.table[0][i // 16] * 16 + i % 16] = c.kv[0][i]
+    c.q.zero_()
+    c.q.view(c.T, 3 * heads, hd)[:, :heads, :3] = 1.0
+    out = c.run()[:new].view(new, heads, hd).float()
+    assert (out[:, :, :4] == 0).all(), out[:, :, :4].abs().max()
