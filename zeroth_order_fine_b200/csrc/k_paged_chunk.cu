@@ -26,8 +26,9 @@
 // Every wait is bounded; on expiry the kernel records the error word, lets what it issued land,
 // frees its tensor memory and returns.
 //
-// Measured: 1024 tokens over 16111 cached, 32 query and 8 kv heads of 128 (279 GFLOP): 254 us, 1.10
-// PFLOP/s, 0.67 of the measured burst peak; back to back under the power cap 298 us.  Of the ~3640
+// Measured: 1024 tokens over 16111 cached, 32 query and 8 kv heads of 128 (279 GFLOP): 264 us, 1.06
+// PFLOP/s, 0.65 of the measured burst peak; back to back under the power cap 304 us.  168 registers a
+// thread, with 32 bytes of spills (head_dim 64: 28 or 32).  Of the ~3640
 // cycles of a unit (clock64 in the roles) each tile's softmax warps work 1670 and wait 1670 for S; the
 // MMAs' own time is 2048, and those of Q K, with both operands in shared memory, take all of its 128
 // bytes a cycle while the next tiles land there.  So the chain softmax -> P V -> Q K of a tile bounds
